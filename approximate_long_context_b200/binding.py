@@ -31,8 +31,11 @@ EXPORTS = [
     "hyper_attn_version", "hyper_attn_profile", "hyper_attn_profile_read",
     "hyper_attn_last_kernel", "hyper_attn_forward_noalloc", "hyper_attn_exact",
     "hyper_attn_diagnostics", "hyper_attn_backward", "hyper_attn_test_fail_alloc",
+    "hyper_attn_prompt", "hyper_attn_prompt_workspace", "hyper_attn_tree", "hyper_attn_tree_workspace",
+    "hyper_attn_cache_free", "hyper_attn_cache_fork", "hyper_attn_cache_workspace", "hyper_attn_cache_reserve",
+    "hyper_attn_cache_append", "hyper_attn_cache_commit",
 ]
-KERNEL_CLASSES = ["hash", "sort", "attn", "causal_base", "draws"]
+KERNEL_CLASSES = ["hash", "sort", "attn", "causal_base", "draws", "prompt", "tree", "cache"]
 
 
 class HAError(RuntimeError):
@@ -54,6 +57,30 @@ class Options(ctypes.Structure):
         ("test_stall_ms", ctypes.c_int),
         ("sampling", ctypes.c_int),
     ]
+
+
+class PromptArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "lse")] + [("tokens", ctypes.c_int64)] +
+                [(n, ctypes.c_int64) for n in ("q_token", "q_head", "k_token", "k_head", "v_token", "v_head", "o_token",
+                                               "o_head")] +
+                [(n, ctypes.c_int) for n in ("heads", "kv_heads", "d")] +
+                [("offsets", ctypes.c_void_p), ("seqs", ctypes.c_int64), ("max_len", ctypes.c_int64),
+                 ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)])
+
+
+class CacheArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "table", "lens", "held", "refs")] +
+                [(n, ctypes.c_int64) for n in ("layers", "pages", "slots", "max_pages")] +
+                [(n, ctypes.c_int) for n in ("kv_heads", "page", "d")])
+
+
+class TreeArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "o", "lse")] + [("tokens", ctypes.c_int64)] +
+                [(n, ctypes.c_int64) for n in ("q_token", "q_head", "o_token", "o_head")] +
+                [("heads", ctypes.c_int), ("layer", ctypes.c_int64)] +
+                [(n, ctypes.c_void_p) for n in ("slots", "offsets", "mask")] +
+                [("seqs", ctypes.c_int64), ("max_draft", ctypes.c_int), ("scale", ctypes.c_float),
+                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)])
 
 
 _lib = None
@@ -91,6 +118,22 @@ def lib():
     L.hyper_attn_last_kernel.argtypes = [vp]
     L.hyper_attn_forward_noalloc.argtypes = [vp, vp, vp, vp, i64, ci, ci, ci, ci, ci, u64, ci, vp]
     L.hyper_attn_profile_read.argtypes = [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ci), ci]
+    st = ctypes.c_size_t
+    L.hyper_attn_prompt.argtypes = [vp, ctypes.POINTER(PromptArgs)]
+    L.hyper_attn_prompt_workspace.argtypes = [i64, i64, ci, ci]
+    L.hyper_attn_prompt_workspace.restype = st
+    cache = ctypes.POINTER(CacheArgs)
+    L.hyper_attn_tree.argtypes = [vp, cache, ctypes.POINTER(TreeArgs)]
+    L.hyper_attn_tree_workspace.argtypes = [vp, ci]
+    L.hyper_attn_tree_workspace.restype = st
+    L.hyper_attn_cache_free.argtypes = [vp, cache, vp, i64]
+    L.hyper_attn_cache_fork.argtypes = [vp, cache, vp, vp, i64]
+    L.hyper_attn_cache_workspace.argtypes = [i64, i64]
+    L.hyper_attn_cache_workspace.restype = st
+    L.hyper_attn_cache_reserve.argtypes = [vp, cache, vp, vp, i64, vp, vp, st]
+    strides = ctypes.POINTER(i64 * 3)
+    L.hyper_attn_cache_append.argtypes = [vp, cache, vp, vp, i64, i64, vp, vp, strides, strides, i64, i64]
+    L.hyper_attn_cache_commit.argtypes = [vp, cache, vp, vp, vp, i64, i64]
     _lib = L
     return L
 
@@ -133,6 +176,49 @@ def _ptr(x) -> int:
     return int(x)
 
 
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _ints(t, device: int, what: str, count=None, bits=32):
+    """The address of a contiguous device tensor of integers."""
+    kind = str(t.dtype)
+    _need(kind == f"torch.int{bits}" and t.is_contiguous() and t.device.type == "cuda" and t.device.index == device,
+          f"{what}: a contiguous int{bits} tensor on the handle's device is needed")
+    _need(count is None or t.numel() == count, f"{what}: {count} values are needed, got {t.numel()}")
+    return t.data_ptr()
+
+
+class PagedCache:
+    """A paged key/value cache in device tensors (ha_cache of the header): k, v [layers, pages, kv_heads, page, d],
+    table [slots, max_pages], lens and held [slots], refs [pages] (int32). The tensors stay the caller's."""
+
+    def __init__(self, k, v, table, lens, held, refs):
+        _need(k.dim() == 5 and k.shape == v.shape and k.dtype == v.dtype, "k and v: [layers, pages, kv_heads, page, d] alike")
+        _need(k.is_contiguous() and v.is_contiguous(), "tensors must be contiguous")
+        _need(k.device.type == "cuda" and v.device == k.device, "the cache must be on one CUDA device")
+        layers, pages, kv_heads, page, d = k.shape
+        slots, max_pages = table.shape
+        device = k.device.index
+        self.k, self.v, self.table, self.lens, self.held, self.refs = k, v, table, lens, held, refs
+        self.device, self.dtype = device, str(k.dtype)
+        self.args = CacheArgs(k.data_ptr(), v.data_ptr(), _ints(table, device, "table"), _ints(lens, device, "lens", slots),
+                              _ints(held, device, "held", slots), _ints(refs, device, "refs", pages), layers, pages, slots,
+                              max_pages, kv_heads, page, d)
+
+    @classmethod
+    def empty(cls, *, layers, pages, kv_heads, page, d, slots, max_pages, dtype="bf16", device=0):
+        """A new cache with all pages free and all slots empty."""
+        import torch
+        dev = torch.device("cuda", device)
+        shape = (layers, pages, kv_heads, page, d)
+        kind = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
+        ints = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)  # noqa: E731
+        return cls(torch.zeros(shape, dtype=kind, device=dev), torch.zeros(shape, dtype=kind, device=dev),
+                   ints(slots, max_pages) - 1, ints(slots), ints(slots), ints(pages))
+
+
 class HyperAttention:
     """One library handle bound to a CUDA device."""
 
@@ -142,6 +228,7 @@ class HyperAttention:
         if rc:
             raise HAError(rc, f"hyper_attn_create(device={device}) failed")
         self.options = default_options()
+        self.device = device
 
     def _check(self, rc: int):
         if rc:
@@ -191,6 +278,126 @@ class HyperAttention:
         """Host buffers (numpy arrays or CPU torch tensors, preferably page-locked); blocks until O is ready."""
         self._check(lib().hyper_attn_forward_host(self._h, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), n, d, heads, block, m,
                                                   r, int(causal), seed))
+
+    # ---- serving: exact attention over packed prompts and over a paged cache, and the cache's steps
+
+    def _rows(self, t, what: str, dtype: int):
+        """[tokens, heads, d] device tensor of the given type, with a contiguous last dimension."""
+        _need(t.dim() == 3 and (t.shape[2] == 1 or t.stride(2) == 1), f"{what}: [tokens, heads, d] with contiguous rows is needed")
+        _need(str(t.dtype) == ("torch.bfloat16" if dtype == 0 else "torch.float32"),
+              f"{what}: the handle's options say {'bf16' if dtype == 0 else 'fp32'}, got {t.dtype}")
+        _need(t.device.type == "cuda" and t.device.index == self.device, f"{what}: on the handle's device")
+        return t.data_ptr(), t.stride(0), t.stride(1)
+
+    def _workspace(self, nbytes: int):
+        """A device buffer whose reuse is ordered by the handle's stream (a graph under capture gets its own)."""
+        import torch
+        stream = self.options.stream or 0
+        if stream == torch.cuda.current_stream(self.device).cuda_stream:
+            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=torch.device("cuda", self.device))
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device) if stream
+                               else torch.cuda.default_stream(self.device)):
+            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=torch.device("cuda", self.device))
+
+    def _out_dtype(self) -> int:
+        return self.options.dtype if self.options.out_dtype < 0 else self.options.out_dtype
+
+    def _lse(self, lse, heads: int, tokens: int):
+        if lse is None:
+            return None
+        _need(tuple(lse.shape) == (heads, tokens) and lse.is_contiguous() and str(lse.dtype) == "torch.float32" and
+              lse.device.type == "cuda" and lse.device.index == self.device,
+              "lse: contiguous fp32 [heads, tokens] on the handle's device is needed")
+        return lse.data_ptr()
+
+    def prompt(self, Q, K, V, O, offsets, *, max_len=None, scale=1.0, lse=None):
+        """Exact causal attention over packed prompts: Q, O [tokens, heads, d], K, V [tokens, kv_heads, d] device tensors
+        (any token and head strides), offsets [seqs + 1] int32; lse [heads, tokens] fp32 is optional. No sequence is
+        longer than max_len (default: tokens). Rows behind the last sequence are left as they are."""
+        dt = self.options.dtype
+        q, k, v = self._rows(Q, "Q", dt), self._rows(K, "K", dt), self._rows(V, "V", dt)
+        o = self._rows(O, "O", self._out_dtype())
+        tokens, heads, d = Q.shape
+        kv_heads = K.shape[1]
+        _need(O.shape == Q.shape and K.shape == V.shape and K.shape[0] == tokens and K.shape[2] == d,
+              "Q, O [tokens, heads, d] and K, V [tokens, kv_heads, d] are needed")
+        _need(offsets.numel() >= 1, "offsets: at least one value is needed")
+        at = _ints(offsets, self.device, "offsets")
+        seqs = offsets.numel() - 1
+        ws = self._workspace(lib().hyper_attn_prompt_workspace(tokens, seqs, heads, kv_heads))
+        a = PromptArgs(q[0], k[0], v[0], o[0], self._lse(lse, heads, tokens), tokens, q[1], q[2], k[1], k[2], v[1], v[2],
+                       o[1], o[2], heads, kv_heads, d, at, seqs, max(tokens, 1) if max_len is None else max_len, scale,
+                       ws.data_ptr(), ws.numel())
+        self._check(lib().hyper_attn_prompt(self._h, ctypes.byref(a)))
+
+    def _cache(self, cache):
+        _need(cache.device == self.device, "the cache must be on the handle's device")
+        _need(cache.dtype == ("torch.bfloat16" if self.options.dtype == 0 else "torch.float32"),
+              f"the cache holds {cache.dtype}, the handle's options say another type")
+        return ctypes.byref(cache.args)
+
+    def tree(self, Q, cache, O, slots, offsets, *, mask=None, max_draft=64, layer=0, scale=1.0, lse=None):
+        """Exact attention of drafted tokens (or single ones) over a PagedCache: sequence i (slot slots[i]; None: slot i) has
+        the rows offsets[i] .. offsets[i+1]-1 of Q and O [tokens, heads, d], whose keys and values were appended behind
+        the slot's committed rows. mask [tokens] int64: bit j of a row lets it see drafted row j (None: rows 0..i)."""
+        c = self._cache(cache)
+        q, o = self._rows(Q, "Q", self.options.dtype), self._rows(O, "O", self._out_dtype())
+        tokens, heads, d = Q.shape
+        _need(O.shape == Q.shape and d == cache.args.d, "Q, O [tokens, heads, d] with the cache's d are needed")
+        _need(offsets.numel() >= 1, "offsets: at least one value is needed")
+        seqs = offsets.numel() - 1
+        ws = self._workspace(lib().hyper_attn_tree_workspace(self._h, d))
+        a = TreeArgs(q[0], o[0], self._lse(lse, heads, tokens), tokens, q[1], q[2], o[1], o[2], heads, layer,
+                     None if slots is None else _ints(slots, self.device, "slots", seqs),
+                     _ints(offsets, self.device, "offsets"),
+                     None if mask is None else _ints(mask, self.device, "mask", tokens, 64), seqs, max_draft, scale,
+                     ws.data_ptr(), ws.numel())
+        self._check(lib().hyper_attn_tree(self._h, c, ctypes.byref(a)))
+
+    def cache_free(self, cache, slots):
+        """Release the pages of the given slots (int32 device tensor) and empty them."""
+        self._check(lib().hyper_attn_cache_free(self._h, self._cache(cache), _ints(slots, self.device, "slots"),
+                                                slots.numel()))
+
+    def cache_fork(self, cache, src, dst):
+        """Make the empty slots dst copies of the slots src; they share the pages of the committed rows."""
+        self._check(lib().hyper_attn_cache_fork(self._h, self._cache(cache), _ints(src, self.device, "src"),
+                                                _ints(dst, self.device, "dst", src.numel()), src.numel()))
+
+    def cache_reserve(self, cache, slots, add, granted=None):
+        """Room for add[i] more rows in slots[i]: new pages, and a copy of a shared last page. granted (int32, optional)
+        gets add[i], or 0 where the free pages did not suffice."""
+        n = slots.numel()
+        ws = self._workspace(lib().hyper_attn_cache_workspace(n, cache.args.pages))
+        self._check(lib().hyper_attn_cache_reserve(
+            self._h, self._cache(cache), _ints(slots, self.device, "slots"), _ints(add, self.device, "add", n), n,
+            None if granted is None else _ints(granted, self.device, "granted", n), ws.data_ptr(), ws.numel()))
+
+    def cache_append(self, cache, slots, offsets, K, V, *, layer=0):
+        """Write K, V [layers, tokens, kv_heads, d] to the cache's layers from `layer` on: rows offsets[i] ..
+        offsets[i+1]-1 go behind the committed rows of slots[i] (reserved before)."""
+        c = self._cache(cache)
+        for t in (K, V):
+            _need(t.dim() == 4 and (t.shape[3] == 1 or t.stride(3) == 1) and str(t.dtype) == cache.dtype and
+                  t.device.type == "cuda" and t.device.index == self.device,
+                  "K, V: [layers, tokens, kv_heads, d] of the cache's type on the handle's device, contiguous rows")
+        _need(K.shape == V.shape and K.shape[2] == cache.args.kv_heads and K.shape[3] == cache.args.d,
+              "K, V: the cache's kv_heads and d are needed")
+        n = slots.numel()
+        strides = [(ctypes.c_int64 * 3)(*t.stride()[:3]) for t in (K, V)]
+        self._check(lib().hyper_attn_cache_append(
+            self._h, c, _ints(slots, self.device, "slots"), _ints(offsets, self.device, "offsets", n + 1), n, K.shape[1],
+            K.data_ptr(), V.data_ptr(), ctypes.byref(strides[0]), ctypes.byref(strides[1]), layer, K.shape[0]))
+
+    def cache_commit(self, cache, slots, counts, keep=None):
+        """Keep counts[i] of the rows behind the committed ones of slots[i]: the rows keep[i, :counts[i]] (ascending), or
+        the first ones; they become committed, the pages behind them are released."""
+        n = slots.numel()
+        if keep is not None:
+            _need(keep.dim() == 2 and keep.shape[0] == n, "keep: [n, max_keep] is needed")
+        self._check(lib().hyper_attn_cache_commit(
+            self._h, self._cache(cache), _ints(slots, self.device, "slots"), _ints(counts, self.device, "counts", n),
+            None if keep is None else _ints(keep, self.device, "keep"), 0 if keep is None else keep.shape[1], n))
 
     def debug_copy(self, what: str, level: int, dtype, count: int) -> np.ndarray:
         out = np.zeros(count, dtype)

@@ -1,63 +1,10 @@
 // ha_api.cu -- the C ABI (include/hyper_attn.h): argument checks, the handle's workspace, the host-side
 // draws and the launch sequence of the forward pass. No step of the method is computed here; every step
 // runs in the kernels of ha_hash.cu, ha_sort.cu, ha_attn_simt.cu and ha_attn_tc.cu.
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
-#include <string>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
-#include "../../include/hyper_attn.h"
-#include "ha_internal.h"
-
-struct hyper_attn_s {
-    int device = 0;
-    ha_options opt{};
-    std::string err;
-    // device workspace (grow-only)
-    unsigned char *ws = nullptr;
-    size_t ws_bytes = 0;
-    // page-locked staging of the draws, and the event that guards its reuse
-    unsigned char *pin = nullptr;
-    size_t pin_bytes = 0;
-    cudaEvent_t pin_free = nullptr;
-    // device copies for hyper_attn_forward_host (grow-only), and its copy streams and chunk events
-    unsigned char *io = nullptr;
-    size_t io_bytes = 0;
-    cudaStream_t cs_in = nullptr, cs_out = nullptr;
-    std::vector<cudaEvent_t> pipe_ev;
-    // test hook: the number of upcoming allocations to fail (hyper_attn_test_fail_alloc)
-    int fail_alloc = 0;
-    // draws currently resident in the workspace, and a host copy of their projection matrix ([d][r]), which the
-    // hash kernel takes as launch parameters
-    bool draws_valid = false;
-    std::vector<float> hostP;
-    uint64_t dk_seed = 0;
-    int dk_d = 0, dk_r = 0, dk_m = 0, dk_causal = 0;
-    int64_t dk_bh = 0, dk_n = 0, dk_base = 0, dk_off = 0;
-    // layout of the last forward (for debug copies)
-    struct Layout {
-        size_t status, P, S, rank, near, lse, perm_tmp, hist, Opart, Lpart, end;
-        std::vector<size_t> perm, inv;
-        std::vector<size_t> perm_bytes;
-        size_t rank_bytes, near_bytes, lse_bytes;
-        // row-norm sampling (0 bytes when off): squared norms, chunk sums, cumulative sums, draws, log weights
-        size_t rn_nrm, rn_csum, rn_cdf, rn_S, rn_lw, rn_bytes;
-    } lay{};
-    bool have_last = false;
-    // the forward pass runs for a backward pass: fp32 O, per-row log normalisers captured (causal: final ones)
-    bool bwd = false;
-    int last_launches = 0;
-    int last_kernel = 0;
-    // profiling: event pairs recorded around kernel-class launches
-    bool profiling = false;
-    std::vector<cudaEvent_t> ev_pool;
-    struct Rec { int cls, launches; size_t e0, e1; };
-    std::vector<Rec> recs;
-    size_t ev_used = 0;
-};
+#include "ha_handle.h"
 
 namespace {
 
@@ -65,39 +12,6 @@ constexpr int kVersion = 100;   // 0.1.0
 constexpr int kDiagMaxN = 16384;   // the diagnostics visit every entry of A
 
 size_t align_up(size_t x, size_t a = 256) { return (x + a - 1) / a * a; }
-
-int fail(hyper_attn_t h, int code, const char *fmt, ...) __attribute__((format(printf, 3, 4)));
-int fail(hyper_attn_t h, int code, const char *fmt, ...) {
-    if (h) {
-        char buf[512];
-        va_list ap;
-        va_start(ap, fmt);
-        vsnprintf(buf, sizeof buf, fmt, ap);
-        va_end(ap);
-        h->err = buf;
-    }
-    return code;
-}
-
-#define HA_CUDA(h, call)                                                                                \
-    do {                                                                                                \
-        cudaError_t e_ = (call);                                                                        \
-        if (e_ != cudaSuccess) return fail((h), HA_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_));  \
-    } while (0)
-
-struct DeviceGuard {
-    int prev = -1;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-        if (prev != dev) cudaSetDevice(dev);
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Causal recursion depth: n <= base -> 0 levels (one exact causal problem); else n = base * 2^L.
 int causal_levels(int64_t n, int64_t base, int *L) {
@@ -381,7 +295,7 @@ int run_forward(hyper_attn_t h, const void *Q, const void *K, const void *V, voi
     // every kernel class's enqueue sits in an NVTX range (a no-op unless a tracing tool is attached); with
     // profiling on, two events from the pool (grown on demand) bracket it on the stream
     static const char *const kRangeName[HA_KC_COUNT] = {"ha:hash", "ha:sort", "ha:attn", "ha:causal_base",
-                                                        "ha:draws"};
+                                                        "ha:draws", "ha:prompt", "ha:tree", "ha:cache"};
     auto prof_begin = [&](int cls) -> long {
         nvtxRangePushA(kRangeName[cls]);
         if (!h->profiling) return -1;
@@ -556,6 +470,14 @@ int hyper_attn_create(hyper_attn_t *out, int device) {
     if (cudaEventCreateWithFlags(&h->pin_free, cudaEventDisableTiming) != cudaSuccess) {
         delete h;
         return HA_ERR_CUDA;
+    }
+    h->sms = prop.multiProcessorCount;
+    if (cudaMalloc(&h->serve_status, 256) != cudaSuccess || cudaMemset(h->serve_status, 0, 256) != cudaSuccess) {
+        cudaGetLastError();
+        if (h->serve_status) cudaFree(h->serve_status);
+        cudaEventDestroy(h->pin_free);
+        delete h;
+        return HA_ERR_OOM;
     }
     *out = h;
     return HA_OK;
@@ -860,15 +782,20 @@ int hyper_attn_status(hyper_attn_t h) {
     if (!h) return HA_ERR_INVALID_ARG;
     DeviceGuard g(h->device);
     HA_CUDA(h, cudaStreamSynchronize(static_cast<cudaStream_t>(h->opt.stream)));
-    if (!h->ws) return HA_OK;
-    int word = 0;
-    HA_CUDA(h, cudaMemcpy(&word, h->ws + h->lay.status, sizeof word, cudaMemcpyDeviceToHost));
+    int word = 0, serve = 0;
+    if (h->ws) HA_CUDA(h, cudaMemcpy(&word, h->ws + h->lay.status, sizeof word, cudaMemcpyDeviceToHost));
+    HA_CUDA(h, cudaMemcpy(&serve, h->serve_status, sizeof serve, cudaMemcpyDeviceToHost));
+    if (word) HA_CUDA(h, cudaMemset(h->ws + h->lay.status, 0, sizeof word));
+    if (serve) HA_CUDA(h, cudaMemset(h->serve_status, 0, sizeof serve));
+    word |= serve;
     if (word) {
-        HA_CUDA(h, cudaMemset(h->ws + h->lay.status, 0, sizeof word));
         if (word & ha::kStatusTimeout) return fail(h, HA_ERR_TIMEOUT, "a device-side wait gave up (status %d)", word);
         if (word & ha::kStatusBounds)
             return fail(h, HA_ERR_CUDA, "a row index read from a permutation or a sample list was out of range, "
                                         "HA_DEBUG build (status %d)", word);
+        if (word & ha::kStatusData)
+            return fail(h, HA_ERR_INVALID_ARG, "an offset, length, slot, page or row index in device memory was out of "
+                                               "range: that sequence was left out (status %d)", word);
         return fail(h, HA_ERR_CUDA, "device status word %d", word);
     }
     return HA_OK;
@@ -919,6 +846,7 @@ int hyper_attn_destroy(hyper_attn_t h) {
         DeviceGuard g(h->device);
         cudaStreamSynchronize(static_cast<cudaStream_t>(h->opt.stream));
         if (h->ws) cudaFree(h->ws);
+        cudaFree(h->serve_status);
         if (h->io) cudaFree(h->io);
         if (h->pin_free) cudaEventSynchronize(h->pin_free);
         if (h->pin) cudaFreeHost(h->pin);

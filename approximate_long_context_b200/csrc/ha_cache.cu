@@ -1,0 +1,501 @@
+// ha_cache.cu -- the steps of the paged key/value cache: freeing, forking, reserving (with the copy of a shared last
+// page), appending and committing (compacting) sequences.
+//
+// All state is in device memory (page table, lengths, pages held, reference counts), so no step waits for the host
+// and all of them can be captured into a graph. A page is free when its reference count is 0; pages are taken
+// lowest index first and in list order, so the same calls always give the same pages. Integer additions are the
+// only atomics; their order changes nothing.
+//
+// What bounds these kernels: the row traffic (each row read once and written once, 16 bytes per thread) for large
+// calls, launch latency and the chain of dependent loads (slot -> length -> page -> row) for small ones.
+#include "ha_common.cuh"
+#include "ha_internal.h"
+#include "ha_serve.cuh"
+
+namespace ha {
+namespace {
+
+// True on every thread of the block when value v occurs in list[0 .. n).
+__device__ __forceinline__ bool block_contains(const int32_t *list, int n, int32_t v) {
+    bool hit = false;
+    for (int j = threadIdx.x; j < n; j += blockDim.x) hit |= list[j] == v;
+    return __syncthreads_or(hit);
+}
+
+__global__ void __launch_bounds__(256) cache_free_kernel(const ServeCache c, const int32_t *slots, int *status) {
+    const int i = blockIdx.x;
+    const int32_t s = slots[i];
+    const bool dup = block_contains(slots, i, s);
+    if (s < 0 || s >= c.slots || dup) {
+        if (threadIdx.x == 0) atomicOr(status, kStatusData);
+        return;
+    }
+    const int held = c.held[s];
+    if (held < 0 || held > c.max_pages) {
+        if (threadIdx.x == 0) atomicOr(status, kStatusData);
+        return;
+    }
+    int32_t *row = c.table + static_cast<int64_t>(s) * c.max_pages;
+    for (int p = threadIdx.x; p < held; p += blockDim.x) {
+        const int32_t id = row[p];
+        if (id >= 0 && id < c.pages) atomicSub(c.refs + id, 1);
+        else atomicOr(status, kStatusData);
+        row[p] = -1;
+    }
+    __syncthreads();   // every thread has read held
+    if (threadIdx.x == 0) {
+        c.held[s] = 0;
+        c.lens[s] = 0;
+    }
+}
+
+// Sources are read as they were before the call: a source that is also a destination of the call is refused.
+__global__ void __launch_bounds__(256) cache_fork_kernel(const ServeCache c, const int32_t *src, const int32_t *dst, int n,
+                                                         int *status) {
+    const int i = blockIdx.x;
+    const int32_t s = src[i], t = dst[i];
+    bool bad = block_contains(dst, i, t);
+    bad |= block_contains(dst, n, s);
+    bad |= s < 0 || s >= c.slots || t < 0 || t >= c.slots;
+    int len = 0, pages = 0;
+    if (!bad) {
+        len = c.lens[s];
+        pages = (len + c.page - 1) >> c.page_shift;
+        bad = len < 0 || pages > c.held[s] || c.held[s] > c.max_pages || c.held[t] != 0 || c.lens[t] != 0;
+    }
+    __syncthreads();   // thread 0 writes the destination's length only after every thread has read it
+    if (bad) {
+        if (threadIdx.x == 0) atomicOr(status, kStatusData);
+        return;
+    }
+    const int32_t *from = c.table + static_cast<int64_t>(s) * c.max_pages;
+    int32_t *to = c.table + static_cast<int64_t>(t) * c.max_pages;
+    for (int p = threadIdx.x; p < pages; p += blockDim.x) {
+        const int32_t id = from[p];
+        if (id >= 0 && id < c.pages) atomicAdd(c.refs + id, 1);
+        else atomicOr(status, kStatusData);
+        to[p] = id;
+    }
+    if (threadIdx.x == 0) {
+        c.lens[t] = len;
+        c.held[t] = pages;
+    }
+}
+
+// Workspace of a reserve call of n entries: per entry the running total of pages needed, the pages held before, the
+// pages to copy (from, to; -1: none) and the rows to copy; then the list of free pages taken.
+struct ReservePlan {
+    int64_t *upto;     // pages needed by entries 0 .. i
+    int32_t *last;     // page that entry i would append to (-1: none)
+    int32_t *held;
+    int32_t *from, *to, *rows;
+    int32_t *ids;
+};
+
+__host__ __device__ inline ReservePlan reserve_plan(void *ws, int n) {
+    ReservePlan p;
+    p.upto = static_cast<int64_t *>(ws);
+    p.last = reinterpret_cast<int32_t *>(p.upto + n);
+    p.held = p.last + n;
+    p.from = p.held + n;
+    p.to = p.from + n;
+    p.rows = p.to + n;
+    p.ids = p.rows + n;
+    return p;
+}
+
+constexpr int kPlanThreads = 1024;
+
+// Inclusive sum over the block; *total gets the block's sum on every thread. scratch: 33 values.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *scratch, int64_t *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();   // the previous call's readers are done
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t w = scratch[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        scratch[lane] = w;
+    }
+    __syncthreads();
+    *total = scratch[31];
+    return x + (warp ? scratch[warp - 1] : 0);
+}
+
+// One block plans the call: what each entry needs, the lowest free pages, and who gets which. One block because the
+// order matters (list order, lowest page first) and the data is small: the scan of the reference counts reads 16 of
+// them per thread and stops as soon as enough free pages are found.
+__global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const ServeCache c, const int32_t *slots,
+                                                                          const int32_t *add, int n, int32_t *granted,
+                                                                          void *ws, int *status) {
+    __shared__ int64_t scratch[33];
+    const ReservePlan p = reserve_plan(ws, n);
+    const int tid = threadIdx.x;
+    // 1. what each entry would append to; an entry out of range, or a slot's second one, asks for nothing
+    for (int i = tid; i < n; i += kPlanThreads) {
+        const int32_t s = slots[i];
+        int last = -1, held = -1;
+        bool ok = s >= 0 && s < c.slots && add[i] >= 0;
+        for (int j = 0; ok && j < i; ++j) ok = slots[j] != s;
+        if (ok) {
+            const int64_t len = c.lens[s];
+            held = c.held[s];
+            const int64_t pages = (len + add[i] + c.page - 1) >> c.page_shift;
+            ok = len >= 0 && held >= 0 && held <= c.max_pages && ((len + c.page - 1) >> c.page_shift) <= held &&
+                 pages <= c.max_pages;
+            if (ok && (len & (c.page - 1)) != 0 && add[i] > 0) {
+                last = c.table[s * c.max_pages + (len >> c.page_shift)];
+                ok = last >= 0 && last < c.pages;
+            }
+        }
+        if (!ok) {
+            atomicOr(status, kStatusData);
+            last = held = -1;
+        }
+        p.last[i] = last;
+        p.held[i] = held;
+    }
+    __syncthreads();
+    // 2. pages needed, in list order: a shared last page is copied by every entry but the last one that holds it
+    int64_t carry = 0;
+    for (int base = 0; base < n; base += kPlanThreads) {
+        const int i = base + tid;
+        int64_t need = 0;
+        if (i < n && p.held[i] >= 0) {
+            const int64_t len = c.lens[slots[i]];
+            const int64_t pages = (len + add[i] + c.page - 1) >> c.page_shift;
+            need = pages > p.held[i] ? pages - p.held[i] : 0;
+            int from = -1;
+            if (p.last[i] >= 0) {
+                const int32_t last = p.last[i];
+                int shared = c.refs[last];
+                if (shared > 1)
+                    for (int j = 0; j < i; ++j) shared -= p.last[j] == last;
+                if (shared > 1) from = last;
+            }
+            p.from[i] = from;
+            p.rows[i] = static_cast<int32_t>(len & (c.page - 1));
+            need += from >= 0;
+        } else if (i < n) {
+            p.from[i] = -1;
+            p.rows[i] = 0;
+        }
+        int64_t total;
+        const int64_t sum = block_scan(need, scratch, &total);
+        if (i < n) {
+            p.upto[i] = carry + sum;
+            p.to[i] = -1;
+        }
+        carry += total;
+    }
+    const int64_t wanted = carry < c.pages ? carry : c.pages;
+    // 3. the lowest free pages
+    int64_t found = 0;
+    for (int64_t base = 0; base < c.pages && found < wanted; base += kPlanThreads * 16) {
+        const int64_t first = base + tid * 16;
+        unsigned free = 0;
+        if (first + 16 <= c.pages) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int4 r = *reinterpret_cast<const int4 *>(c.refs + first + 4 * q);
+                free |= static_cast<unsigned>((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << (4 * q);
+            }
+        } else {
+            for (int q = 0; q < 16; ++q)
+                if (first + q < c.pages && c.refs[first + q] == 0) free |= 1u << q;
+        }
+        int64_t total;
+        int64_t at = found + block_scan(__popc(free), scratch, &total) - __popc(free);
+        while (free && at < wanted) {
+            p.ids[at++] = static_cast<int32_t>(first + __ffs(free) - 1);
+            free &= free - 1;
+        }
+        found += total;
+    }
+    if (found > wanted) found = wanted;
+    __syncthreads();
+    // 4. a prefix of the list is served: the entries whose running total the free pages cover
+    for (int i = tid; i < n; i += kPlanThreads) {
+        const bool ok = p.held[i] >= 0 && p.upto[i] <= found;
+        if (granted) granted[i] = ok ? add[i] : 0;
+        if (!ok) p.from[i] = -1;
+        if (ok) {
+            const int32_t s = slots[i];
+            const int64_t pages = (static_cast<int64_t>(c.lens[s]) + add[i] + c.page - 1) >> c.page_shift;
+            if (pages > p.held[i]) c.held[s] = static_cast<int32_t>(pages);
+        }
+    }
+    __syncthreads();
+    for (int64_t t = tid; t < found; t += kPlanThreads) {
+        int lo = 0, hi = n - 1;   // the entry that page t goes to: the first whose running total exceeds t
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (p.upto[mid] > t) hi = mid;
+            else lo = mid + 1;
+        }
+        const int i = lo;
+        if (p.upto[i] > found) continue;   // not served
+        const int64_t start = i ? p.upto[i - 1] : 0;
+        const int32_t s = slots[i], id = p.ids[t];
+        int64_t j = t - start;
+        int32_t *row = c.table + s * c.max_pages;
+        c.refs[id] = 1;
+        if (p.from[i] >= 0 && j == 0) {
+            row[c.lens[s] >> c.page_shift] = id;
+            atomicSub(c.refs + p.from[i], 1);
+            p.to[i] = id;
+        } else {
+            j -= p.from[i] >= 0;
+            row[p.held[i] + j] = id;
+        }
+    }
+}
+
+// The committed rows of a shared last page go to its copy: one block per (entry, layer, k or v).
+__global__ void __launch_bounds__(256) cache_reserve_copy_kernel(const ServeCache c, int esz, int n, void *ws) {
+    grid_dependency_wait();
+    const ReservePlan p = reserve_plan(ws, n);
+    const int from = p.from[blockIdx.x], to = p.to[blockIdx.x];
+    if (from < 0 || to < 0) return;
+    const int64_t layer = blockIdx.y >> 1;
+    char *base = static_cast<char *>((blockIdx.y & 1) ? c.v : c.k);
+    const int64_t row_bytes = static_cast<int64_t>(c.d) * esz, head_bytes = row_bytes * c.page,
+                  page_bytes = head_bytes * c.kv_heads;
+    const char *src = base + (layer * c.pages + from) * page_bytes;
+    char *dst = base + (layer * c.pages + to) * page_bytes;
+    const int per_head = static_cast<int>(p.rows[blockIdx.x] * row_bytes / 16);
+    const int total = per_head * c.kv_heads;
+    for (int x0 = threadIdx.x; x0 < total; x0 += 256 * 4) {
+        int4 buf[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int x = x0 + 256 * u;
+            if (x < total) buf[u] = *reinterpret_cast<const int4 *>(src + (x / per_head) * head_bytes + (x % per_head) * 16);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int x = x0 + 256 * u;
+            if (x < total) *reinterpret_cast<int4 *>(dst + (x / per_head) * head_bytes + (x % per_head) * 16) = buf[u];
+        }
+    }
+}
+
+struct AppendArgs {
+    const char *k, *v;
+    int64_t kl, kt, kh, vl, vt, vh;   // strides in bytes: layer, token, head
+    int64_t layer, layers;
+};
+
+constexpr int kAppendLayers = 4;   // layers per block
+
+// One block per token and group of layers: the place is looked up once, then the rows are copied.
+__global__ void __launch_bounds__(256) cache_append_kernel(const ServeCache c, int esz, const int32_t *slots,
+                                                           const int32_t *cu, int n, int64_t tokens, const AppendArgs a,
+                                                           int *status) {
+    const int64_t t = blockIdx.x;
+    // the sequence that holds token t: the last one whose offset is not behind it
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid + 1] > t) hi = mid;
+        else lo = mid + 1;
+    }
+    if (lo >= n) return;   // behind the last sequence
+    const int64_t start = cu[lo];
+    if (t < start) {
+        if (threadIdx.x == 0) atomicOr(status, kStatusData);
+        return;
+    }
+    const int32_t s = slots[lo];
+    if (s < 0 || s >= c.slots) {
+        if (threadIdx.x == 0) atomicOr(status, kStatusData);
+        return;
+    }
+    const int64_t len = c.lens[s], at = len + t - start, pi = at >> c.page_shift;
+    const int held = c.held[s];
+    int32_t id = -1;
+    if (len >= 0 && pi < held && held <= c.max_pages) id = c.table[s * c.max_pages + pi];
+    if (id < 0 || id >= c.pages || c.refs[id] != 1) {   // a page that another slot shares is not written
+        if (threadIdx.x == 0) atomicOr(status, kStatusData);
+        return;
+    }
+    const int64_t row_bytes = static_cast<int64_t>(c.d) * esz, head_bytes = row_bytes * c.page,
+                  page_bytes = head_bytes * c.kv_heads;
+    const int per_row = static_cast<int>(row_bytes / 16), per_layer = per_row * c.kv_heads;
+    const int64_t l0 = static_cast<int64_t>(blockIdx.y) * kAppendLayers;
+    const int nl = static_cast<int>(min(static_cast<int64_t>(kAppendLayers), a.layers - l0));
+    const int total = per_layer * nl * 2;
+    const int64_t off = (at & (c.page - 1)) * row_bytes;
+    for (int x0 = threadIdx.x; x0 < total; x0 += 256 * 4) {
+        int4 buf[4];
+        char *dst[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int x = x0 + 256 * u;
+            dst[u] = nullptr;
+            if (x >= total) continue;
+            const int kv = x / (per_layer * nl), y = x - kv * per_layer * nl;
+            const int l = y / per_layer, z = y - l * per_layer, h = z / per_row, w = z - h * per_row;
+            const char *src = kv ? a.v + (l0 + l) * a.vl + t * a.vt + h * a.vh : a.k + (l0 + l) * a.kl + t * a.kt + h * a.kh;
+            buf[u] = *reinterpret_cast<const int4 *>(src + w * 16);
+            dst[u] = static_cast<char *>(kv ? c.v : c.k) + ((a.layer + l0 + l) * c.pages + id) * page_bytes +
+                     h * head_bytes + off + w * 16;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (dst[u]) *reinterpret_cast<int4 *>(dst[u]) = buf[u];
+    }
+}
+
+// Whether entry i of a commit is valid; the whole block takes part. *len, *held, *count of the slot.
+__device__ bool commit_entry(const ServeCache &c, const int32_t *slots, const int32_t *counts, const int32_t *keep,
+                             int64_t max_keep, int i, int *len, int *held, int *count) {
+    const int32_t s = slots[i];
+    bool bad = block_contains(slots, i, s) || s < 0 || s >= c.slots;
+    if (bad) return false;
+    *len = c.lens[s];
+    *held = c.held[s];
+    *count = counts[i];
+    const int64_t room = static_cast<int64_t>(*held) * c.page - *len;
+    if (*len < 0 || *held < 0 || *held > c.max_pages || *count < 0 || *count > room || (keep && *count > max_keep))
+        return false;
+    if (keep) {
+        const int32_t *mine = keep + i * max_keep;
+        for (int j = threadIdx.x; j < *count; j += blockDim.x) {
+            const int32_t x = mine[j];
+            bad |= x < 0 || x >= room || (j > 0 && x <= mine[j - 1]);
+        }
+    }
+    // the pages that rows are read from and written to
+    const int32_t *row = c.table + s * c.max_pages;
+    for (int p = (*len >> c.page_shift) + threadIdx.x; p < *held; p += blockDim.x) bad |= row[p] < 0 || row[p] >= c.pages;
+    return !__syncthreads_or(bad);
+}
+
+constexpr int kMoveChunk = 256;   // kept rows staged at a time
+
+// The kept rows of a draft move to the front of it: row len + keep[i] -> len + i, one block per (entry, layer, k or v).
+// keep is ascending, so keep[i] >= i and a row is read before a later row is written over it; every thread moves its
+// own 16-byte column in ascending order, eight rows in flight.
+__global__ void __launch_bounds__(128) cache_commit_move_kernel(const ServeCache c, int esz, const int32_t *slots,
+                                                                const int32_t *counts, const int32_t *keep,
+                                                                int64_t max_keep) {
+    __shared__ int64_t from[kMoveChunk], to[kMoveChunk];   // byte offsets of the rows in a layer, head 0
+    int len = 0, held = 0, count = 0;
+    if (!commit_entry(c, slots, counts, keep, max_keep, blockIdx.x, &len, &held, &count)) return;   // flagged below
+    const int32_t *mine = keep + static_cast<int64_t>(blockIdx.x) * max_keep;
+    const int32_t *row = c.table + static_cast<int64_t>(slots[blockIdx.x]) * c.max_pages;
+    const int64_t row_bytes = static_cast<int64_t>(c.d) * esz, head_bytes = row_bytes * c.page,
+                  page_bytes = head_bytes * c.kv_heads;
+    const int64_t layer = blockIdx.y >> 1;
+    char *base = static_cast<char *>((blockIdx.y & 1) ? c.v : c.k) + layer * c.pages * page_bytes;
+    const int per_row = static_cast<int>(row_bytes / 16), total = per_row * c.kv_heads;
+    for (int first = 0; first < count; first += kMoveChunk) {
+        const int m = min(kMoveChunk, count - first);
+        __syncthreads();
+        for (int j = threadIdx.x; j < m; j += blockDim.x) {
+            const int64_t a = static_cast<int64_t>(len) + mine[first + j], b = static_cast<int64_t>(len) + first + j;
+            from[j] = row[a >> c.page_shift] * page_bytes + (a & (c.page - 1)) * row_bytes;
+            to[j] = row[b >> c.page_shift] * page_bytes + (b & (c.page - 1)) * row_bytes;
+        }
+        __syncthreads();
+        for (int x = threadIdx.x; x < total; x += blockDim.x) {
+            char *col = base + (x / per_row) * head_bytes + (x % per_row) * 16;
+            for (int j0 = 0; j0 < m; j0 += 8) {
+                int4 buf[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (j0 + u < m && from[j0 + u] != to[j0 + u]) buf[u] = *reinterpret_cast<const int4 *>(col + from[j0 + u]);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (j0 + u < m && from[j0 + u] != to[j0 + u]) *reinterpret_cast<int4 *>(col + to[j0 + u]) = buf[u];
+            }
+        }
+    }
+}
+
+// Lengths grow by the kept rows; the pages behind the new length are released.
+__global__ void __launch_bounds__(128) cache_commit_kernel(const ServeCache c, const int32_t *slots, const int32_t *counts,
+                                                           const int32_t *keep, int64_t max_keep, int *status) {
+    grid_dependency_wait();
+    int len = 0, held = 0, count = 0;
+    if (!commit_entry(c, slots, counts, keep, max_keep, blockIdx.x, &len, &held, &count)) {
+        if (threadIdx.x == 0) atomicOr(status, kStatusData);
+        return;
+    }
+    const int32_t s = slots[blockIdx.x];
+    int32_t *row = c.table + static_cast<int64_t>(s) * c.max_pages;
+    const int after = (len + count + c.page - 1) >> c.page_shift;
+    for (int p = after + threadIdx.x; p < held; p += blockDim.x) {
+        atomicSub(c.refs + row[p], 1);
+        row[p] = -1;
+    }
+    if (threadIdx.x == 0) {
+        c.lens[s] = len + count;
+        c.held[s] = after;
+    }
+}
+
+}  // namespace
+
+size_t cache_workspace(int64_t n, int64_t pages) {
+    return static_cast<size_t>(n) * (sizeof(int64_t) + 5 * sizeof(int32_t)) + static_cast<size_t>(pages) * sizeof(int32_t);
+}
+
+int launch_cache_free(const ServeCache &c, const int32_t *slots, int n, int *status, cudaStream_t st) {
+    cache_free_kernel<<<n, 256, 0, st>>>(c, slots, status);
+    return cudaPeekAtLastError() == cudaSuccess ? 1 : -1;
+}
+
+int launch_cache_fork(const ServeCache &c, const int32_t *src, const int32_t *dst, int n, int *status, cudaStream_t st) {
+    cache_fork_kernel<<<n, 256, 0, st>>>(c, src, dst, n, status);
+    return cudaPeekAtLastError() == cudaSuccess ? 1 : -1;
+}
+
+int launch_cache_reserve(const ServeCache &c, int esz, const int32_t *slots, const int32_t *add, int n, int32_t *granted,
+                         void *ws, int *status, cudaStream_t st) {
+    cache_reserve_plan_kernel<<<1, kPlanThreads, 0, st>>>(c, slots, add, n, granted, ws, status);
+    if (cudaPeekAtLastError() != cudaSuccess) return -1;
+    const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(2 * c.layers));
+    return launch_dependent(cache_reserve_copy_kernel, grid, dim3(256), 0, st, c, esz, n, ws) ? 2 : -1;
+}
+
+int launch_cache_append(const ServeCache &c, int esz, const int32_t *slots, const int32_t *cu, int n, int64_t tokens,
+                        const void *k, const void *v, const int64_t kstr[3], const int64_t vstr[3], int64_t layer,
+                        int64_t layers, int *status, cudaStream_t st) {
+    AppendArgs a;
+    a.k = static_cast<const char *>(k);
+    a.v = static_cast<const char *>(v);
+    a.kl = kstr[0] * esz; a.kt = kstr[1] * esz; a.kh = kstr[2] * esz;
+    a.vl = vstr[0] * esz; a.vt = vstr[1] * esz; a.vh = vstr[2] * esz;
+    a.layer = layer;
+    a.layers = layers;
+    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>((layers + kAppendLayers - 1) / kAppendLayers));
+    cache_append_kernel<<<grid, 256, 0, st>>>(c, esz, slots, cu, n, tokens, a, status);
+    return cudaPeekAtLastError() == cudaSuccess ? 1 : -1;
+}
+
+int launch_cache_commit(const ServeCache &c, int esz, const int32_t *slots, const int32_t *counts, const int32_t *keep,
+                        int64_t max_keep, int n, int *status, cudaStream_t st) {
+    int launches = 0;
+    if (keep) {
+        const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(2 * c.layers));
+        cache_commit_move_kernel<<<grid, 128, 0, st>>>(c, esz, slots, counts, keep, max_keep);
+        if (cudaPeekAtLastError() != cudaSuccess) return -1;
+        ++launches;
+    }
+    if (!launch_dependent(cache_commit_kernel, dim3(n), dim3(128), 0, st, c, slots, counts, keep, max_keep, status)) return -1;
+    return launches + 1;
+}
+
+}  // namespace ha

@@ -14,6 +14,7 @@ constexpr int kSortWarps = 8;
 // Device status word bits (written by kernels that wait with a bound, read by hyper_attn_status).
 constexpr int kStatusTimeout = 1;
 constexpr int kStatusBounds = 2;     // HA_DEBUG builds: a row index read from data was out of range
+constexpr int kStatusData = 4;       // serving: an offset, length, slot, page or row index in device memory was bad
 
 // One level of the computation. Level 0 is the non-causal problem (one node covering all n rows);
 // causal level l >= 1 has nodes of node_len = n >> (l-1) rows whose off-diagonal problem pairs the
@@ -114,6 +115,65 @@ int launch_bwd_level(const Level &lv, const void *Q, const void *K, const void *
 int launch_bwd_leaf(const void *Q, const void *K, const void *V, const void *dO, int dtype, int64_t bh, int64_t n,
                     int d, int64_t leaf, const float *L, const float *g, float *dQ, float *dK, float *dV,
                     cudaStream_t st);
+
+// ---- serving: packed prompts, drafted trees over a paged cache, the cache's own steps ----
+
+struct ServeCache {
+    void *k, *v;                 // [layers][pages][kv_heads][page][d]
+    int32_t *table;              // [slots][max_pages], -1: none
+    int32_t *lens, *held;        // [slots]
+    int32_t *refs;               // [pages]
+    int64_t layers, pages, slots, max_pages;
+    int kv_heads, page, page_shift, d;
+};
+
+// Arguments of the prompt and tree attention kernels. Rows of one key head's queries are numbered
+// token * group + (head - kv_head * group) within a sequence, so that the query heads that share a key head also
+// share its key tiles.
+struct ServeArgs {
+    const void *q, *k, *v;       // tree: k and v are unused, the cache's layer is kp, vp
+    void *o;
+    float *lse;                  // [heads][tokens] or null
+    int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head, o_tok, o_head;   // strides in elements
+    int64_t tokens;
+    int heads, kv_heads, group, d;
+    const int32_t *cu;           // [seqs + 1]
+    int seqs;
+    int max_len;                 // longest sequence (prompt) or draft (tree) the caller promises
+    float scale;
+    int out_dtype;
+    int *status;
+    // tree
+    const void *kp, *vp;
+    const int32_t *slots;        // [seqs] or null (sequence i is slot i)
+    const int64_t *mask;         // [tokens] or null (chain)
+    const int32_t *table, *lens, *held;
+    int64_t pages, max_slots, max_pages;
+    int page_shift;
+    // workspace: prompt: the list of work items; tree: descriptors and partial results of split segments
+    void *ws;
+    size_t ws_bytes;
+    int sms;
+};
+
+size_t serve_prompt_workspace(int64_t tokens, int64_t seqs, int group);
+size_t serve_tree_workspace(int sms, int d);
+// Return the number of kernels launched, -1 on a launch error.
+int launch_prompt_simt(const ServeArgs &a, int dtype, cudaStream_t st);
+int launch_tree_simt(const ServeArgs &a, int dtype, cudaStream_t st);
+// The second kernel of a tree call on `blocks` blocks with at most `rows` query rows per tile.
+bool launch_tree_join(const ServeArgs &a, int blocks, int rows, cudaStream_t st);
+
+size_t cache_workspace(int64_t n, int64_t pages);
+int launch_cache_free(const ServeCache &c, const int32_t *slots, int n, int *status, cudaStream_t st);
+int launch_cache_fork(const ServeCache &c, const int32_t *src, const int32_t *dst, int n, int *status, cudaStream_t st);
+int launch_cache_reserve(const ServeCache &c, int esz, const int32_t *slots, const int32_t *add, int n, int32_t *granted,
+                         void *ws, int *status, cudaStream_t st);
+int launch_cache_append(const ServeCache &c, int esz, const int32_t *slots, const int32_t *cu, int n, int64_t tokens,
+                        const void *k, const void *v, const int64_t kstr[3], const int64_t vstr[3], int64_t layer,
+                        int64_t layers, int *status, cudaStream_t st);
+int launch_cache_commit(const ServeCache &c, int esz, const int32_t *slots, const int32_t *counts, const int32_t *keep,
+                        int64_t max_keep, int n, int *status, cudaStream_t st);
 
 // ---- host-side draws (ha_draws.cpp) ----
 void draw_projection(uint64_t seed, int d, int r, float *P);

@@ -1,0 +1,214 @@
+// ha_serve.cuh -- device helpers of the serving kernels: dependent launches, the walk over packed sequences and the
+// partition of the tree attention's key tiles.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ha_internal.h"
+
+namespace ha {
+
+// A kernel launched with launch_dependent may start before the kernel in front of it on the stream has ended; it calls
+// this before it touches memory that the other one reads or writes (returns once that kernel and its writes are done).
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launch behind the previous kernel of the stream without waiting for its last block to drain first (programmatic
+// stream serialisation); the kernel must call grid_dependency_wait. True on success.
+template <typename... P, typename... A>
+inline bool launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess;
+}
+
+// Sequence i of a prompt call: its first row and length; length 0 and a flag where the offsets are not ascending
+// rows of the call or the sequence is longer than promised.
+__device__ __forceinline__ bool prompt_seq(const ServeArgs &a, int i, int *start, int *len) {
+    const int64_t s = a.cu[i], e = a.cu[i + 1];
+    const bool ok = s >= 0 && e >= s && e <= a.tokens && e - s <= a.max_len;
+    *start = ok ? static_cast<int>(s) : 0;
+    *len = ok ? static_cast<int>(e - s) : 0;
+    return ok;
+}
+
+// Sequence i of a tree call: first query row, drafted rows t, committed rows len, its row of the page table. t = 0
+// (and a flag) where something is out of range.
+struct TreeSeq {
+    int start, t, len;
+    int64_t table;
+};
+__device__ __forceinline__ bool tree_seq(const ServeArgs &a, int i, TreeSeq *x) {
+    const int64_t s = a.cu[i], e = a.cu[i + 1];
+    const int64_t slot = a.slots ? a.slots[i] : i;
+    x->start = 0;
+    x->t = 0;
+    x->len = 0;
+    x->table = 0;
+    if (s < 0 || e < s || e > a.tokens || e - s > a.max_len || slot < 0 || slot >= a.max_slots) return false;
+    if (e == s) return true;
+    const int64_t len = a.lens[slot], held = a.held[slot];
+    if (len < 0 || held > a.max_pages || ((len + (e - s) + (int64_t(1) << a.page_shift) - 1) >> a.page_shift) > held)
+        return false;
+    x->start = static_cast<int>(s);
+    x->t = static_cast<int>(e - s);
+    x->len = static_cast<int>(len);
+    x->table = slot * a.max_pages;
+    return true;
+}
+
+// A contiguous run of key tiles of one segment (a sequence, a key head and a tile of query rows) that one block works
+// on. The segments' key tiles are numbered one segment after the other and cut into equal shares, one per block, so
+// that long and short sequences keep every SM busy alike; a segment cut by a share's border is joined afterwards.
+struct TreePiece {
+    int seq, kh, tile;   // tile: index of the query-row tile
+    TreeSeq x;
+    int nk;              // key tiles of the segment
+    int k0, k1;          // the piece: key tiles [k0, k1)
+    int64_t total;       // key tiles of the call
+    int shares;          // blocks that have some
+    int64_t end;         // number behind the segment's last key tile
+};
+
+// Descriptor of a segment that starts in block c and ends in a later one: what the joining kernel needs.
+struct TreeJoin {
+    int pieces;          // 0: nothing to join for this block
+    int start;           // first query row of the sequence
+    int row0, rows;      // rows of the tile within the sequence (token * group + head), how many
+    int kh;
+    int pad[3];
+};
+
+// Partial results: slot 2c is the piece that block c continues, slot 2c + 1 the one it begins and does not end.
+// A slot has `rows` rows of d fp32 numerators (relative to the row's maximum), then maxima (base 2), then sums.
+constexpr int kTreeSlotRows = 128;
+
+__host__ __device__ inline size_t tree_slot_floats(int d) { return static_cast<size_t>(kTreeSlotRows) * (d + 2); }
+
+__device__ __forceinline__ TreeJoin *tree_joins(void *ws) { return static_cast<TreeJoin *>(ws); }
+__device__ __forceinline__ float *tree_slot(void *ws, int blocks, int slot, int d) {
+    return reinterpret_cast<float *>(static_cast<char *>(ws) + sizeof(TreeJoin) * blocks) + slot * tree_slot_floats(d);
+}
+
+// The walk of one block over its share, run by one whole warp. rows_per_tile: tokens of a query tile times group (SIMT:
+// flattened rows, tok_tile 0) or whole tokens (tok_tile tokens).
+struct TreeWalk {
+    int64_t total;         // key tiles of the call
+    int shares;            // blocks that get some: no share is empty, so a segment's pieces are in neighbouring blocks
+    int64_t first, last;   // this block's, in the segments' numbering
+    int64_t at;            // next one
+    int seq;               // sequence of `at`
+    int64_t seq_first;     // number of its first key tile
+    TreeSeq x;
+    int nk, tiles;
+
+    static __device__ __forceinline__ int tiles_of(const ServeArgs &a, const TreeSeq &x, int tile_rows, int tok_tile) {
+        return tok_tile ? (x.t + tok_tile - 1) / tok_tile : (x.t * a.group + tile_rows - 1) / tile_rows;
+    }
+    static __device__ __forceinline__ int64_t cost(const ServeArgs &a, const TreeSeq &x, int key_tile, int tile_rows,
+                                                   int tok_tile) {
+        if (x.t == 0) return 0;
+        return static_cast<int64_t>(a.kv_heads) * tiles_of(a, x, tile_rows, tok_tile) *
+               ((x.len + x.t + key_tile - 1) / key_tile);
+    }
+    __device__ __forceinline__ void begin(const ServeArgs &a, int key_tile, int tile_rows, int tok_tile, int block,
+                                          int blocks) {
+        const int lane = threadIdx.x & 31;
+        total = 0;
+        bool ok = true;
+        for (int b = 0; b < a.seqs; b += 32) {
+            TreeSeq y;
+            y.t = 0;
+            if (b + lane < a.seqs) ok &= tree_seq(a, b + lane, &y);
+            total += cost(a, y, key_tile, tile_rows, tok_tile);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (!ok && block == 0) atomicOr(a.status, kStatusData);
+        shares = static_cast<int>(min(total, static_cast<int64_t>(blocks)));
+        first = block < shares ? total * block / shares : 0;
+        last = block < shares ? total * (block + 1) / shares : 0;
+        at = first;
+        seq = a.seqs;
+        seq_first = 0;
+        if (first == last) return;
+        // the sequence that holds `first`
+        int64_t run = 0;
+        for (int b = 0; b < a.seqs; b += 32) {
+            TreeSeq y;
+            y.t = 0;
+            if (b + lane < a.seqs) tree_seq(a, b + lane, &y);
+            const int64_t mine = cost(a, y, key_tile, tile_rows, tok_tile);
+            int64_t sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t z = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += z;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, run + sum > first);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                seq = b + l;
+                seq_first = run + __shfl_sync(0xffffffffu, sum - mine, l);
+                break;
+            }
+            run += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        load(a, key_tile, tile_rows, tok_tile);
+    }
+    __device__ __forceinline__ void load(const ServeArgs &a, int key_tile, int tile_rows, int tok_tile) {
+        tree_seq(a, seq, &x);
+        nk = x.t ? (x.len + x.t + key_tile - 1) / key_tile : 0;
+        tiles = tiles_of(a, x, tile_rows, tok_tile);
+    }
+    // The next piece of the share; false at its end. Row tiles vary fastest, then key heads: segments that read the
+    // same keys are neighbours.
+    __device__ __forceinline__ bool next(const ServeArgs &a, int key_tile, int tile_rows, int tok_tile, TreePiece *p) {
+        if (at >= last) return false;
+        while (at - seq_first >= static_cast<int64_t>(a.kv_heads) * tiles * nk) {
+            seq_first += static_cast<int64_t>(a.kv_heads) * tiles * nk;
+            ++seq;
+            if (seq >= a.seqs) return false;
+            load(a, key_tile, tile_rows, tok_tile);
+        }
+        const int64_t off = at - seq_first;
+        const int64_t segment = off / nk;
+        p->seq = seq;
+        p->x = x;
+        p->nk = nk;
+        p->tile = static_cast<int>(segment % tiles);
+        p->kh = static_cast<int>(segment / tiles);
+        p->k0 = static_cast<int>(off - segment * nk);
+        const int64_t left = last - at;
+        p->k1 = static_cast<int>(min(static_cast<int64_t>(nk), p->k0 + left));
+        p->total = total;
+        p->shares = shares;
+        p->end = at - p->k0 + nk;
+        at += p->k1 - p->k0;
+        return true;
+    }
+};
+
+// Blocks that share the segment of which `p` (begun and not ended by `block`) is the first piece.
+__device__ __forceinline__ int tree_pieces(const TreePiece &p, int block) {
+    int n = 1;   // the blocks behind it whose share begins before the segment's end
+    while (block + n < p.shares && p.total * (block + n) / p.shares < p.end) ++n;
+    return n;
+}
+
+// The mask of drafted rows that query token i (of t) sees, bit j for drafted row j.
+__device__ __forceinline__ uint64_t tree_bits(const ServeArgs &a, int start, int i, int t) {
+    const uint64_t all = t >= 64 ? ~0ull : (1ull << t) - 1;
+    if (a.mask) return static_cast<uint64_t>(a.mask[start + i]) & all;
+    return (i >= 63 ? ~0ull : (1ull << (i + 1)) - 1) & all;
+}
+
+}  // namespace ha

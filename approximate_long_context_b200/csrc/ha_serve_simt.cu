@@ -1,0 +1,492 @@
+// ha_serve_simt.cu -- exact softmax attention for serving in fp32 arithmetic: packed prompts (causal, grouped heads)
+// and trees of drafted tokens over a paged cache. The path for fp32 tensors, and for bf16 ones when the SIMT family is
+// asked for. Also the kernel that joins the tree segments cut by a block's share (both families).
+//
+// One block: 64 query rows (row = token * group + head within its key head) against 64 keys at a time, one online
+// softmax: m' = max(m, max_j x_j), l' = l 2^(m - m') + sum_j 2^(x_j - m'), O' = O 2^(m - m') + sum_j 2^(x_j - m') v_j with
+// x_j = scale log2(e) q.k_j; O = O / l, L = (m + log2 l) ln 2. 128 threads, 8 rows x 4 keys each for the scores and
+// 8 rows x d/16 columns for the product with V: 12 (16) 16-byte shared loads feed 128 (256) fused multiply-adds, so the
+// FP32 pipes and not shared memory bound it. Sums, maxima and numerators are fp32.
+//
+// A value row of a masked key can hold an infinity or NaN and must not reach the rows that do not see it (0 * inf):
+// the load of a tile votes on non-finite values, and a tile with one and a mask takes the product with a select.
+#include <math.h>
+
+#include "ha_common.cuh"
+#include "ha_internal.h"
+#include "ha_serve.cuh"
+
+namespace ha {
+namespace {
+
+constexpr int kBM = 64, kBN = 64, kThreads = 128;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float *p) {
+    return *reinterpret_cast<const float4 *>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<uint16_t>(const uint16_t *p) {
+    const uint2 r = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xffff0000u));
+}
+
+__device__ __forceinline__ bool finite4(float4 v) {
+    // |v| < inf is false for infinities and NaN
+    return fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY && fabsf(v.w) < INFINITY;
+}
+
+template <int D>
+struct Smem {
+    static constexpr int LD = D + 4;      // row pitch: 16-byte aligned, eight consecutive rows on different banks
+    static constexpr int LP = kBN + 4;
+    static constexpr int kQ = 0;
+    static constexpr int kK = kBM * LD;   // P overwrites K once the scores are done
+    static constexpr int kV = kK + kBN * LD;
+    static constexpr int kFloats = kV + kBN * LD;
+    static constexpr int kBytes = kFloats * 4;
+    static_assert(kBM * LP <= kBN * LD, "P fits in K's place");
+};
+
+// What one block works on: rows [row0, row0 + rows) of sequence rows, key head kh, key tiles [k0, k1).
+struct Work {
+    int start, t, len;    // first query row, query tokens, keys in front of the first query token (prompt: 0)
+    int row0, rows, kh;
+    int k0, k1;
+    int64_t table;
+};
+
+template <int D, bool TREE, typename T>
+__device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float *sm, float (&acc)[8][D / 16], float (&m)[8],
+                                       float (&l)[8]) {
+    using S = Smem<D>;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    float *Qs = sm + S::kQ, *Ks = sm + S::kK, *Ps = Ks, *Vs = sm + S::kV;
+    const float c = a.scale * kLog2e;
+    const T *q = static_cast<const T *>(a.q);
+    __syncthreads();   // the previous piece's reads are done
+    for (int x = tid; x < kBM * (D / 4); x += kThreads) {
+        const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < w.rows) {
+            const int row = w.row0 + r, tok = row / a.group, head = w.kh * a.group + row - tok * a.group;
+            v = load4<T>(q + static_cast<int64_t>(w.start + tok) * a.q_tok + static_cast<int64_t>(head) * a.q_head + col);
+        }
+        *reinterpret_cast<float4 *>(Qs + r * S::LD + col) = v;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) acc[i][j] = 0.f;
+    }
+    int tok[8];
+    uint64_t bits[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = min(w.rows - 1, ty * 8 + i);
+        tok[i] = (w.row0 + r) / a.group;
+        bits[i] = TREE ? tree_bits(a, w.start, tok[i], w.t) : 0;
+    }
+    const int keys = w.len + w.t;
+    // the first key that some row of the tile does not see
+    const int masked_from = TREE ? w.len : w.row0 / a.group + 1;
+    for (int kt = w.k0; kt < w.k1; ++kt) {
+        const int base = kt * kBN;
+        __syncthreads();   // the previous tile's P and V have been read
+        bool odd = false;
+        for (int x = tid; x < kBN * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+            float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+            if (base + r < keys) {
+                int64_t ko, vo;
+                const T *kp, *vp;
+                bool ok = true;
+                if (TREE) {
+                    const int key = base + r;
+                    const int32_t page = a.table[w.table + (key >> a.page_shift)];
+                    ok = page >= 0 && page < a.pages;
+                    if (!ok) atomicOr(a.status, kStatusData);
+                    const int64_t at = ((static_cast<int64_t>(page) * a.kv_heads + w.kh) << a.page_shift) +
+                                       (key & ((1 << a.page_shift) - 1));
+                    ko = vo = at * D + col;
+                    kp = static_cast<const T *>(a.kp);
+                    vp = static_cast<const T *>(a.vp);
+                } else {
+                    const int64_t row = w.start + base + r;
+                    ko = row * a.k_tok + w.kh * a.k_head + col;
+                    vo = row * a.v_tok + w.kh * a.v_head + col;
+                    kp = static_cast<const T *>(a.k);
+                    vp = static_cast<const T *>(a.v);
+                }
+                if (ok) {
+                    kv = load4<T>(kp + ko);
+                    vv = load4<T>(vp + vo);
+                }
+            }
+            odd |= !finite4(vv);
+            *reinterpret_cast<float4 *>(Ks + r * S::LD + col) = kv;
+            *reinterpret_cast<float4 *>(Vs + r * S::LD + col) = vv;
+        }
+        const bool masked = base + kBN > masked_from || base + kBN > keys;
+        const bool select = __syncthreads_or(odd) && masked;
+        float s[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 2
+        for (int k = 0; k < D; k += 4) {
+            float4 kf[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kf[j] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * j) * S::LD + k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 qf = *reinterpret_cast<const float4 *>(Qs + (ty * 8 + i) * S::LD + k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = fmaf(qf.x, kf[j].x, s[i][j]);
+                    s[i][j] = fmaf(qf.y, kf[j].y, s[i][j]);
+                    s[i][j] = fmaf(qf.z, kf[j].z, s[i][j]);
+                    s[i][j] = fmaf(qf.w, kf[j].w, s[i][j]);
+                }
+            }
+        }
+        __syncthreads();   // K has been read: P may take its place
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float top = -INFINITY;
+            unsigned seen = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = base + tx + 16 * j;
+                bool see;
+                if (TREE) see = key < w.len || (key < keys && (bits[i] >> (key - w.len) & 1));
+                else see = key <= tok[i];
+                seen |= static_cast<unsigned>(see || !masked) << j;
+                s[i][j] *= c;
+                if (seen >> j & 1) top = fmaxf(top, s[i][j]);
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float mn = fmaxf(m[i], top);
+            const float ref = mn == -INFINITY ? 0.f : mn;   // nothing seen so far: no -inf - -inf
+            const float corr = exp2f(m[i] - ref);
+            m[i] = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = seen >> j & 1 ? exp2f(s[i][j] - ref) : 0.f;
+                sum += p;
+                Ps[(ty * 8 + i) * S::LP + tx + 16 * j] = p;
+            }
+            l[i] = l[i] * corr + sum;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) acc[i][j] *= corr;
+        }
+        __syncwarp();   // a row's P is written and read by the same half warp
+        if (!select) {
+#pragma unroll 1
+            for (int k = 0; k < kBN; k += 4) {
+                float4 p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i] = *reinterpret_cast<const float4 *>(Ps + (ty * 8 + i) * S::LP + k);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int g = 0; g < D / 64; ++g) {
+                        const float4 v = *reinterpret_cast<const float4 *>(Vs + (k + kk) * S::LD + g * 64 + tx * 4);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float pk = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                            acc[i][g * 4 + 0] = fmaf(pk, v.x, acc[i][g * 4 + 0]);
+                            acc[i][g * 4 + 1] = fmaf(pk, v.y, acc[i][g * 4 + 1]);
+                            acc[i][g * 4 + 2] = fmaf(pk, v.z, acc[i][g * 4 + 2]);
+                            acc[i][g * 4 + 3] = fmaf(pk, v.w, acc[i][g * 4 + 3]);
+                        }
+                    }
+            }
+        } else {
+            for (int k = 0; k < kBN; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float pk = Ps[(ty * 8 + i) * S::LP + k];
+#pragma unroll
+                    for (int g = 0; g < D / 64; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float v = Vs[k * S::LD + g * 64 + tx * 4 + e];
+                            if (pk != 0.f) acc[i][g * 4 + e] = fmaf(pk, v, acc[i][g * 4 + e]);
+                        }
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+}
+
+// O = numerator / sum; a row that sees nothing (sum 0) is 0 with L = -inf.
+template <int D>
+__device__ __forceinline__ void write_rows(const ServeArgs &a, const Work &w, const float (&acc)[8][D / 16],
+                                           const float (&m)[8], const float (&l)[8]) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = ty * 8 + i;
+        if (r >= w.rows) continue;
+        const int row = w.row0 + r, tok = row / a.group, head = w.kh * a.group + row - tok * a.group;
+        const int64_t at = static_cast<int64_t>(w.start + tok) * a.o_tok + static_cast<int64_t>(head) * a.o_head;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g) {
+            float o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = l[i] == 0.f ? 0.f : acc[i][g * 4 + e] * inv;
+            const int64_t x = at + g * 64 + tx * 4;
+            if (a.out_dtype == 0) {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
+                uint2 u;
+                u.x = *reinterpret_cast<const uint32_t *>(&lo);
+                u.y = *reinterpret_cast<const uint32_t *>(&hi);
+                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + x) = u;
+            } else {
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + x) = make_float4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        if (a.lse && tx == 0)
+            a.lse[static_cast<int64_t>(head) * a.tokens + w.start + tok] =
+                l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+    }
+}
+
+// Block b: key head b mod kv_heads of the (b / kv_heads)-th 64-row tile, the tiles counted over the sequences.
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const ServeArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    __shared__ Work shared;
+    const int kh = static_cast<int>(blockIdx.x % a.kv_heads);
+    const int64_t want = blockIdx.x / a.kv_heads;
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int64_t run = 0;
+        int found = -1, tile = 0;
+        bool ok = true;
+        for (int b = 0; b < a.seqs; b += 32) {
+            int start = 0, len = 0;
+            if (b + lane < a.seqs) ok &= prompt_seq(a, b + lane, &start, &len);
+            const int64_t mine = (static_cast<int64_t>(len) * a.group + kBM - 1) / kBM;
+            int64_t sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t z = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += z;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, run + sum > want);
+            if (found < 0 && hit) {
+                const int s = __ffs(hit) - 1;
+                found = b + s;
+                tile = static_cast<int>(want - run - __shfl_sync(0xffffffffu, sum - mine, s));
+            }
+            run += __shfl_sync(0xffffffffu, sum, 31);
+            if (found >= 0 && blockIdx.x != 0) break;   // block 0 looks all sequences over
+        }
+        if (!ok && blockIdx.x == 0) atomicOr(a.status, kStatusData);
+        if (lane == 0) {
+            Work w{};
+            w.rows = 0;
+            if (found >= 0) {
+                int start, len;
+                prompt_seq(a, found, &start, &len);
+                // a sequence's last (most expensive) tile first
+                const int tiles = static_cast<int>((static_cast<int64_t>(len) * a.group + kBM - 1) / kBM);
+                w.start = start;
+                w.t = len;
+                w.len = 0;
+                w.row0 = (tiles - 1 - tile) * kBM;
+                w.rows = min(kBM, len * a.group - w.row0);
+                w.kh = kh;
+                w.k0 = 0;
+                w.k1 = ((w.row0 + w.rows - 1) / a.group) / kBN + 1;
+            }
+            shared = w;
+        }
+    }
+    __syncthreads();
+    const Work w = shared;
+    if (w.rows <= 0) return;
+    float acc[8][D / 16], m[8], l[8];
+    attend<D, false, T>(a, w, sm, acc, m, l);
+    write_rows<D>(a, w, acc, m, l);
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads) tree_simt_kernel(const ServeArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    __shared__ TreePiece piece;
+    __shared__ int more;
+    TreeWalk walk;
+    const int warp = threadIdx.x >> 5, blocks = gridDim.x, block = blockIdx.x;
+    if (warp == 0) walk.begin(a, kBN, kBM, 0, block, blocks);
+    if (threadIdx.x == 0) tree_joins(a.ws)[block].pieces = 0;
+    for (;;) {
+        __syncthreads();
+        if (warp == 0) {
+            TreePiece p;
+            const bool got = walk.next(a, kBN, kBM, 0, &p);
+            if (threadIdx.x == 0) {
+                piece = p;
+                more = got;
+            }
+        }
+        __syncthreads();
+        if (!more) break;
+        Work w;
+        w.start = piece.x.start;
+        w.t = piece.x.t;
+        w.len = piece.x.len;
+        w.table = piece.x.table;
+        w.row0 = piece.tile * kBM;
+        w.rows = min(kBM, w.t * a.group - w.row0);
+        w.kh = piece.kh;
+        w.k0 = piece.k0;
+        w.k1 = piece.k1;
+        float acc[8][D / 16], m[8], l[8];
+        attend<D, true, T>(a, w, sm, acc, m, l);
+        if (piece.k0 == 0 && piece.k1 == piece.nk) {
+            write_rows<D>(a, w, acc, m, l);
+            continue;
+        }
+        const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+        float *slot = tree_slot(a.ws, blocks, 2 * block + (piece.k0 == 0), D);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = ty * 8 + i;
+            if (r >= w.rows) continue;
+#pragma unroll
+            for (int g = 0; g < D / 64; ++g)
+                *reinterpret_cast<float4 *>(slot + r * D + g * 64 + tx * 4) =
+                    make_float4(acc[i][g * 4], acc[i][g * 4 + 1], acc[i][g * 4 + 2], acc[i][g * 4 + 3]);
+            if (tx == 0) {
+                slot[kTreeSlotRows * D + r] = m[i];
+                slot[kTreeSlotRows * (D + 1) + r] = l[i];
+            }
+        }
+        if (piece.k0 == 0 && threadIdx.x == 0) {
+            TreeJoin j{};
+            j.pieces = tree_pieces(piece, block);
+            j.start = w.start;
+            j.row0 = w.row0;
+            j.rows = w.rows;
+            j.kh = w.kh;
+            tree_joins(a.ws)[block] = j;
+        }
+    }
+}
+
+// Joins the pieces of the segment that block blockIdx.x begins and does not end: one warp per row, the pieces' numerators
+// and sums weighted with 2^(m_piece - m). The order is fixed, so equal calls give equal bits.
+constexpr int kJoinRows = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinRows) tree_join_kernel(const ServeArgs a, int blocks) {
+    grid_dependency_wait();
+    const TreeJoin j = tree_joins(a.ws)[blockIdx.x];
+    const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (j.pieces == 0 || r >= j.rows) return;
+    constexpr int C = D / 32;
+    auto slot_of = [&](int i) {
+        return tree_slot(a.ws, blocks, i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i), D);
+    };
+    float m = -INFINITY;
+    for (int i = lane; i < j.pieces; i += 32) m = fmaxf(m, slot_of(i)[kTreeSlotRows * D + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float acc[C], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < C; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < j.pieces; ++i) {
+        const float *s = slot_of(i);
+        const float w = exp2f(s[kTreeSlotRows * D + r] - ref);
+        l += w * s[kTreeSlotRows * (D + 1) + r];
+        float v[C];
+        if (C == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(s + r * D + lane * 4);
+        else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(s + r * D + lane * 2);
+#pragma unroll
+        for (int e = 0; e < C; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+    }
+    const int row = j.row0 + r, tok = row / a.group, head = j.kh * a.group + row - tok * a.group;
+    const int64_t at = static_cast<int64_t>(j.start + tok) * a.o_tok + static_cast<int64_t>(head) * a.o_head + lane * C;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (a.out_dtype == 0) {
+#pragma unroll
+        for (int e = 0; e < C; e += 2)
+            *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.o) + at + e) =
+                __floats2bfloat162_rn(l == 0.f ? 0.f : acc[e] * inv, l == 0.f ? 0.f : acc[e + 1] * inv);
+    } else {
+#pragma unroll
+        for (int e = 0; e < C; ++e) static_cast<float *>(a.o)[at + e] = l == 0.f ? 0.f : acc[e] * inv;
+    }
+    if (a.lse && lane == 0)
+        a.lse[static_cast<int64_t>(head) * a.tokens + j.start + tok] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+}
+
+template <typename K>
+bool allow_smem(K kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+
+template <int D, typename T>
+int prompt_simt(const ServeArgs &a, cudaStream_t st) {
+    if (!allow_smem(prompt_simt_kernel<D, T>, Smem<D>::kBytes)) return -1;
+    if ((a.tokens * a.group / kBM + a.seqs) * a.kv_heads > 0x7fffffff) return -2;   // blocks of a grid
+    const int64_t tiles = a.tokens * a.group / kBM + a.seqs;   // at most: one ragged tile per sequence
+    prompt_simt_kernel<D, T><<<static_cast<unsigned>(tiles * a.kv_heads), kThreads, Smem<D>::kBytes, st>>>(a);
+    return cudaPeekAtLastError() == cudaSuccess ? 1 : -1;
+}
+
+template <int D, typename T>
+int tree_simt(const ServeArgs &a, cudaStream_t st) {
+    if (!allow_smem(tree_simt_kernel<D, T>, Smem<D>::kBytes)) return -1;
+    const int blocks = 2 * a.sms;   // two per SM fit (shared memory)
+    tree_simt_kernel<D, T><<<blocks, kThreads, Smem<D>::kBytes, st>>>(a);
+    if (cudaPeekAtLastError() != cudaSuccess) return -1;
+    const int rows = a.max_len * a.group < kBM ? a.max_len * a.group : kBM;
+    return launch_tree_join(a, blocks, rows, st) ? 2 : -1;
+}
+
+}  // namespace
+
+bool launch_tree_join(const ServeArgs &a, int blocks, int rows, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows));
+    return a.d == 64 ? launch_dependent(tree_join_kernel<64>, grid, dim3(32 * kJoinRows), 0, st, a, blocks)
+                     : launch_dependent(tree_join_kernel<128>, grid, dim3(32 * kJoinRows), 0, st, a, blocks);
+}
+
+size_t serve_prompt_workspace(int64_t, int64_t, int) { return 0; }
+
+size_t serve_tree_workspace(int sms, int d) {
+    const size_t blocks = 2 * static_cast<size_t>(sms);
+    return blocks * sizeof(TreeJoin) + 2 * blocks * tree_slot_floats(d) * sizeof(float);
+}
+
+int launch_prompt_simt(const ServeArgs &a, int dtype, cudaStream_t st) {
+    if (a.d == 64) return dtype == 0 ? prompt_simt<64, uint16_t>(a, st) : prompt_simt<64, float>(a, st);
+    return dtype == 0 ? prompt_simt<128, uint16_t>(a, st) : prompt_simt<128, float>(a, st);
+}
+
+int launch_tree_simt(const ServeArgs &a, int dtype, cudaStream_t st) {
+    if (a.d == 64) return dtype == 0 ? tree_simt<64, uint16_t>(a, st) : tree_simt<64, float>(a, st);
+    return dtype == 0 ? tree_simt<128, uint16_t>(a, st) : tree_simt<128, float>(a, st);
+}
+
+}  // namespace ha

@@ -215,7 +215,8 @@ HA_API int hyper_attn_debug_copy(hyper_attn_t h, int what, int level, void *host
 /* Synchronise the handle's stream and report device-side status: HA_OK, HA_ERR_TIMEOUT if a bounded
  * wait gave up, or HA_ERR_CUDA if the stream holds an error or (HA_DEBUG build, libhyper_attn_debug.so) a
  * tensor-core kernel read a row index out of range from a permutation or a sample list (it then read row 0
- * instead). Clears the device status word. */
+ * instead), or HA_ERR_INVALID_ARG if a serving call met an entry out of range in device memory. Clears the
+ * device status words. */
 HA_API int hyper_attn_status(hyper_attn_t h);
 
 /* Kernel classes for profiling. */
@@ -225,13 +226,16 @@ typedef enum {
     HA_KC_ATTN = 2,        /* block + sampled attention of one level, including the gather and the merge */
     HA_KC_CAUSAL_BASE = 3, /* exact causal leaves and the final log-space merge */
     HA_KC_DRAWS = 4,       /* row-norm draws on the device (norms, cumulative sums, draws) */
-    HA_KC_COUNT = 5
+    HA_KC_PROMPT = 5,      /* attention over packed prompts */
+    HA_KC_TREE = 6,        /* attention of drafted tokens over the cache */
+    HA_KC_CACHE = 7,       /* the cache's own steps */
+    HA_KC_COUNT = 8
 } ha_kernel_class;
 
 /* enable = 1: record a CUDA event pair on the handle's stream around every kernel class launch of the
  * following forward calls; 0: stop recording. Recording adds two event records per launch.
  * Independently of this switch, the host-side enqueue of every kernel class sits in an NVTX range named
- * "ha:hash", "ha:sort", "ha:attn", "ha:causal_base" or "ha:draws", which tracing tools (Nsight Systems) show
+ * "ha:hash", "ha:sort", "ha:attn", "ha:causal_base", "ha:draws", "ha:prompt", "ha:tree" or "ha:cache", which tracing tools (Nsight Systems) show
  * next to the kernels; without such a tool attached the ranges cost a few nanoseconds. */
 HA_API int hyper_attn_profile(hyper_attn_t h, int enable);
 
@@ -283,6 +287,117 @@ HA_API int hyper_attn_destroy(hyper_attn_t h);
  */
 HA_API int hyper_attn_forward_noalloc(const void *Q, const void *K, const void *V, void *O, int64_t n, int d,
                                       int heads, int block, int m, int r, uint64_t seed, int dtype, void *stream);
+
+/* ------------------------------------------------------------------------------------------------ serving
+ *
+ * Exact softmax attention next to the approximation, in the forms that serving a model needs: prompts of
+ * different lengths packed behind one another, query heads that share key heads, and drafted (or single)
+ * tokens over a paged key/value cache, with the cache's own steps. Common to all of them:
+ *   - Types: the handle's dtype for Q, K, V and the cache (HA_DTYPE_BF16 or HA_DTYPE_FP32), its out_dtype for
+ *     O; fp32 log normalisers. d = 64 or 128. Kernel family by the handle's option: AUTO takes the tensor-core
+ *     kernels for bf16 and the SIMT fp32 kernels for fp32, SIMT the latter for both, TC refuses fp32. The
+ *     tensor-core kernels round the softmax weights to bf16 before the product with V (sums stay fp32);
+ *     the SIMT kernels keep them in fp32.
+ *   - Q and O are [tokens, heads, d], K and V [tokens, kv_heads, d], with strides in elements for tokens and
+ *     heads (the last dimension is contiguous; strides of 16-byte multiples). heads is a multiple of kv_heads,
+ *     at most 128 query heads share one key head; query head h reads key head h / (heads / kv_heads).
+ *   - `scale` (> 0) multiplies q.k inside exp.
+ *   - Offsets, lengths, slots, masks and page tables are device memory and are read when the kernels run. An
+ *     entry out of range leaves its sequence out (nothing of it is written) and makes hyper_attn_status report
+ *     HA_ERR_INVALID_ARG; nothing is read or written out of bounds.
+ *   - A row whose scores are all masked or -inf gives O = 0 and a log normaliser of -inf. Infinities and NaN
+ *     in keys and values that a row does not see do not reach it.
+ *   - Rows of O (and of the log normalisers) behind the last sequence are left as they are.
+ *   - Nothing is allocated and nothing waits for the host: every call can be captured into a graph. Workspaces
+ *     belong to the caller (16-byte aligned, contents undefined, free for reuse once the call has run);
+ *     calls that may run at the same time, graphs on different streams among them, need workspaces of their
+ *     own. The handle's status word is shared by all of them.
+ *   - Equal calls give equal bits.
+ */
+
+/* Causal attention over packed prompts: row i of a sequence sees rows 0..i of the same sequence. */
+typedef struct {
+    const void *q, *k, *v;
+    void *o;                          /* no overlap with q, k, v */
+    float *lse;                       /* [heads, tokens] log normaliser, or NULL */
+    int64_t tokens;                   /* rows of q, k, v, o; 0 is allowed (nothing is done); <= 2^30 */
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;   /* strides in elements */
+    int heads, kv_heads, d;
+    const int32_t *offsets;           /* device, [seqs + 1], ascending: sequence s is rows offsets[s] .. offsets[s+1]-1 */
+    int64_t seqs;                     /* <= 2^20; empty sequences are allowed */
+    int64_t max_len;                  /* no sequence is longer than this */
+    float scale;
+    void *workspace;                  /* hyper_attn_prompt_workspace bytes */
+    size_t workspace_bytes;
+} ha_prompt_args;
+HA_API size_t hyper_attn_prompt_workspace(int64_t tokens, int64_t seqs, int heads, int kv_heads);
+HA_API int hyper_attn_prompt(hyper_attn_t h, const ha_prompt_args *args);
+
+/* A paged key/value cache in the caller's device memory. Slot s holds one sequence: its committed rows
+ * 0 .. lens[s]-1 and, between a reserve and a commit, room for more in the same pages; row j lies in page
+ * table[s][j / page]. A page is free when refs is 0; sequences that were forked share pages. */
+typedef struct {
+    void *k, *v;                      /* [layers, pages, kv_heads, page, d] of the handle's dtype, 16-byte aligned */
+    int32_t *table;                   /* [slots, max_pages], -1 where there is no page */
+    int32_t *lens;                    /* [slots] committed rows */
+    int32_t *held;                    /* [slots] pages in the slot's row of the table */
+    int32_t *refs;                    /* [pages] slots that hold the page, 16-byte aligned */
+    int64_t layers, pages, slots, max_pages;   /* max_pages * page <= 2^30, pages < 2^31, layers <= 16384 */
+    int kv_heads, page, d;            /* page: 16, 32, 64, 128 or 256 rows */
+} ha_cache;
+
+/* Attention of drafted tokens over the cache. Sequence i (slot slots[i]) has the query rows offsets[i] ..
+ * offsets[i+1]-1, at most 64; their keys and values are rows lens, lens + 1, .. of the slot (reserved and
+ * appended before). Query row i sees every committed row and the drafted rows of its own sequence whose bit is
+ * set in mask (bit j: drafted row j); a tree is the masks of each token's ancestors and itself. One row
+ * per sequence is ordinary decoding. */
+typedef struct {
+    const void *q;
+    void *o;                          /* no overlap with q or the cache */
+    float *lse;                       /* [heads, tokens] or NULL */
+    int64_t tokens;
+    int64_t q_token, q_head, o_token, o_head;
+    int heads;                        /* a multiple of the cache's kv_heads */
+    int64_t layer;                    /* layer of the cache */
+    const int32_t *slots;             /* device, [seqs], or NULL: sequence i is slot i */
+    const int32_t *offsets;           /* device, [seqs + 1] */
+    const int64_t *mask;              /* device, [tokens], or NULL: drafted rows 0..i (a chain) */
+    int64_t seqs;                     /* <= 65536 */
+    int max_draft;                    /* 1..64: no sequence has more rows */
+    float scale;
+    void *workspace;                  /* hyper_attn_tree_workspace bytes */
+    size_t workspace_bytes;
+} ha_tree_args;
+HA_API size_t hyper_attn_tree_workspace(hyper_attn_t h, int d);
+HA_API int hyper_attn_tree(hyper_attn_t h, const ha_cache *cache, const ha_tree_args *args);
+
+/* The cache's steps; n entries (n = 0: nothing is done), all lists in device memory. A slot named twice in one
+ * call counts once (the first time) and is reported by hyper_attn_status like an entry out of range.
+ *   free     releases the pages of slots[i] and empties the slot.
+ *   fork     dst[i] (an empty slot) becomes a copy of src[i]: it shares the pages of the committed rows. Sources
+ *            are read as they were before the call; a source that is also a destination is refused.
+ *   reserve  makes room for add[i] more rows behind the committed ones of slots[i] (which replaces, not adds to, the
+ *            room of an earlier reserve that was not committed): takes the lowest free pages, in list order, and
+ *            replaces a shared, partly filled last page by a copy of its committed rows in all layers. The entries
+ *            that the free pages cover are a prefix of the list; granted[i] (optional) is add[i] for those and 0
+ *            for the others, which are left as they were (status is not set for them).
+ *            Workspace: hyper_attn_cache_workspace bytes.
+ *   append   writes rows k, v [layers, tokens, kv_heads, d] (strides in elements: layer, token, head) to layers
+ *            layer .. layer + layers - 1, row t of sequence i to its committed length + t. Lengths do not change. A row
+ *            whose page is missing or shared (no reserve since the fork) is left out and reported.
+ *   commit   keeps counts[i] of the rows behind the committed ones: row length + keep[i][j] moves to
+ *            length + j (keep [n, max_keep], strictly ascending in each row's first counts[i] entries; NULL: the
+ *            first counts[i] rows, nothing moves), the length grows by counts[i], pages behind it are released. */
+HA_API int hyper_attn_cache_free(hyper_attn_t h, const ha_cache *cache, const int32_t *slots, int64_t n);
+HA_API int hyper_attn_cache_fork(hyper_attn_t h, const ha_cache *cache, const int32_t *src, const int32_t *dst, int64_t n);
+HA_API size_t hyper_attn_cache_workspace(int64_t n, int64_t pages);
+HA_API int hyper_attn_cache_reserve(hyper_attn_t h, const ha_cache *cache, const int32_t *slots, const int32_t *add,
+                                    int64_t n, int32_t *granted, void *workspace, size_t workspace_bytes);
+HA_API int hyper_attn_cache_append(hyper_attn_t h, const ha_cache *cache, const int32_t *slots, const int32_t *offsets,
+                                   int64_t n, int64_t tokens, const void *k, const void *v, const int64_t k_strides[3],
+                                   const int64_t v_strides[3], int64_t layer, int64_t layers);
+HA_API int hyper_attn_cache_commit(hyper_attn_t h, const ha_cache *cache, const int32_t *slots, const int32_t *counts,
+                                   const int32_t *keep, int64_t max_keep, int64_t n);
 
 /* Library version as major*10000 + minor*100 + patch. */
 HA_API int hyper_attn_version(void);
