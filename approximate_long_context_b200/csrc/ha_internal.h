@@ -161,7 +161,9 @@ size_t serve_tree_workspace(int sms, int d);
 // Return the number of kernels launched, -1 on a launch error.
 int launch_prompt_simt(const ServeArgs &a, int dtype, cudaStream_t st);
 int launch_tree_simt(const ServeArgs &a, int dtype, cudaStream_t st);
-// The second kernel of a tree call on `blocks` blocks with at most `rows` query rows per tile.
+int launch_prompt_tc(const ServeArgs &a, cudaStream_t st);
+int launch_tree_tc(const ServeArgs &a, cudaStream_t st);
+// The second kernel of a tree call on `blocks` blocks whose segments have at most `rows` query rows.
 bool launch_tree_join(const ServeArgs &a, int blocks, int rows, cudaStream_t st);
 
 size_t cache_workspace(int64_t n, int64_t pages);

@@ -88,14 +88,14 @@ struct TreeJoin {
 };
 
 // Partial results: slot 2c is the piece that block c continues, slot 2c + 1 the one it begins and does not end.
-// A slot has `rows` rows of d fp32 numerators (relative to the row's maximum), then maxima (base 2), then sums.
-constexpr int kTreeSlotRows = 128;
-
-__host__ __device__ inline size_t tree_slot_floats(int d) { return static_cast<size_t>(kTreeSlotRows) * (d + 2); }
+// A slot has `rows` rows of d fp32 numerators (relative to the row's maximum), then maxima (base 2), then sums; rows is
+// the largest number of query rows of a segment.
+__host__ __device__ inline size_t tree_slot_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 2); }
 
 __device__ __forceinline__ TreeJoin *tree_joins(void *ws) { return static_cast<TreeJoin *>(ws); }
-__device__ __forceinline__ float *tree_slot(void *ws, int blocks, int slot, int d) {
-    return reinterpret_cast<float *>(static_cast<char *>(ws) + sizeof(TreeJoin) * blocks) + slot * tree_slot_floats(d);
+__device__ __forceinline__ float *tree_slot(void *ws, int blocks, int slot, int rows, int d) {
+    return reinterpret_cast<float *>(static_cast<char *>(ws) + sizeof(TreeJoin) * blocks) +
+           slot * tree_slot_floats(rows, d);
 }
 
 // The walk of one block over its share, run by one whole warp. rows_per_tile: tokens of a query tile times group (SIMT:

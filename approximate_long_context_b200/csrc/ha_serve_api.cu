@@ -52,7 +52,7 @@ int check_strides(hyper_attn_t h, const char *what, int64_t tokens, int heads, i
 }
 
 int pick_family(hyper_attn_t h, bool *tc) {
-    *tc = false;
+    *tc = h->opt.kernel != HA_KERNEL_SIMT && h->opt.dtype == HA_DTYPE_BF16;
     if (h->opt.kernel == HA_KERNEL_TC && h->opt.dtype != HA_DTYPE_BF16)
         return fail(h, HA_ERR_UNSUPPORTED, "tensor-core kernels need bf16 inputs");
     return HA_OK;
@@ -140,7 +140,7 @@ int hyper_attn_prompt(hyper_attn_t h, const ha_prompt_args *p) {
         a.sms = h->sms;
         cudaStream_t st = static_cast<cudaStream_t>(h->opt.stream);
         ProfScope prof(h, HA_KC_PROMPT, "ha:prompt", st);
-        const int k = ha::launch_prompt_simt(a, h->opt.dtype, st);
+        const int k = tc ? ha::launch_prompt_tc(a, st) : ha::launch_prompt_simt(a, h->opt.dtype, st);
         prof.end(k);
         return launched(h, k, "prompt attention");
     });
@@ -202,7 +202,7 @@ int hyper_attn_tree(hyper_attn_t h, const ha_cache *cache, const ha_tree_args *p
         a.sms = h->sms;
         cudaStream_t st = static_cast<cudaStream_t>(h->opt.stream);
         ProfScope prof(h, HA_KC_TREE, "ha:tree", st);
-        const int k = ha::launch_tree_simt(a, h->opt.dtype, st);
+        const int k = tc ? ha::launch_tree_tc(a, st) : ha::launch_tree_simt(a, h->opt.dtype, st);
         prof.end(k);
         return launched(h, k, "tree attention");
     });

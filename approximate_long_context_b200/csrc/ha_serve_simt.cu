@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const ServeArgs a) 
             continue;
         }
         const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-        float *slot = tree_slot(a.ws, blocks, 2 * block + (piece.k0 == 0), D);
+        float *slot = tree_slot(a.ws, blocks, 2 * block + (piece.k0 == 0), kBM, D);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = ty * 8 + i;
@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const ServeArgs a) 
                 *reinterpret_cast<float4 *>(slot + r * D + g * 64 + tx * 4) =
                     make_float4(acc[i][g * 4], acc[i][g * 4 + 1], acc[i][g * 4 + 2], acc[i][g * 4 + 3]);
             if (tx == 0) {
-                slot[kTreeSlotRows * D + r] = m[i];
-                slot[kTreeSlotRows * (D + 1) + r] = l[i];
+                slot[kBM * D + r] = m[i];
+                slot[kBM * (D + 1) + r] = l[i];
             }
         }
         if (piece.k0 == 0 && threadIdx.x == 0) {
@@ -396,17 +396,17 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const ServeArgs a) 
 constexpr int kJoinRows = 4;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinRows) tree_join_kernel(const ServeArgs a, int blocks) {
+__global__ void __launch_bounds__(32 * kJoinRows) tree_join_kernel(const ServeArgs a, int blocks, int rows) {
     grid_dependency_wait();
     const TreeJoin j = tree_joins(a.ws)[blockIdx.x];
     const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (j.pieces == 0 || r >= j.rows) return;
     constexpr int C = D / 32;
     auto slot_of = [&](int i) {
-        return tree_slot(a.ws, blocks, i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i), D);
+        return tree_slot(a.ws, blocks, i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i), rows, D);
     };
     float m = -INFINITY;
-    for (int i = lane; i < j.pieces; i += 32) m = fmaxf(m, slot_of(i)[kTreeSlotRows * D + r]);
+    for (int i = lane; i < j.pieces; i += 32) m = fmaxf(m, slot_of(i)[rows * D + r]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float ref = m == -INFINITY ? 0.f : m;
@@ -416,8 +416,8 @@ __global__ void __launch_bounds__(32 * kJoinRows) tree_join_kernel(const ServeAr
 #pragma unroll 4
     for (int i = 0; i < j.pieces; ++i) {
         const float *s = slot_of(i);
-        const float w = exp2f(s[kTreeSlotRows * D + r] - ref);
-        l += w * s[kTreeSlotRows * (D + 1) + r];
+        const float w = exp2f(s[rows * D + r] - ref);
+        l += w * s[rows * (D + 1) + r];
         float v[C];
         if (C == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(s + r * D + lane * 4);
         else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(s + r * D + lane * 2);
@@ -460,23 +460,23 @@ int tree_simt(const ServeArgs &a, cudaStream_t st) {
     const int blocks = 2 * a.sms;   // two per SM fit (shared memory)
     tree_simt_kernel<D, T><<<blocks, kThreads, Smem<D>::kBytes, st>>>(a);
     if (cudaPeekAtLastError() != cudaSuccess) return -1;
-    const int rows = a.max_len * a.group < kBM ? a.max_len * a.group : kBM;
-    return launch_tree_join(a, blocks, rows, st) ? 2 : -1;
+    return launch_tree_join(a, blocks, kBM, st) ? 2 : -1;
 }
 
 }  // namespace
 
 bool launch_tree_join(const ServeArgs &a, int blocks, int rows, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows));
-    return a.d == 64 ? launch_dependent(tree_join_kernel<64>, grid, dim3(32 * kJoinRows), 0, st, a, blocks)
-                     : launch_dependent(tree_join_kernel<128>, grid, dim3(32 * kJoinRows), 0, st, a, blocks);
+    const int used = a.max_len * a.group < rows ? a.max_len * a.group : rows;
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((used + kJoinRows - 1) / kJoinRows));
+    return a.d == 64 ? launch_dependent(tree_join_kernel<64>, grid, dim3(32 * kJoinRows), 0, st, a, blocks, rows)
+                     : launch_dependent(tree_join_kernel<128>, grid, dim3(32 * kJoinRows), 0, st, a, blocks, rows);
 }
 
-size_t serve_prompt_workspace(int64_t, int64_t, int) { return 0; }
-
 size_t serve_tree_workspace(int sms, int d) {
-    const size_t blocks = 2 * static_cast<size_t>(sms);
-    return blocks * sizeof(TreeJoin) + 2 * blocks * tree_slot_floats(d) * sizeof(float);
+    // SIMT: two blocks per SM of 64 rows; tensor cores: one of up to 256 rows
+    const size_t simt = 2 * static_cast<size_t>(sms) * (sizeof(TreeJoin) + 2 * tree_slot_floats(kBM, d) * sizeof(float));
+    const size_t tc = static_cast<size_t>(sms) * (sizeof(TreeJoin) + 2 * tree_slot_floats(256, d) * sizeof(float));
+    return simt > tc ? simt : tc;
 }
 
 int launch_prompt_simt(const ServeArgs &a, int dtype, cudaStream_t st) {

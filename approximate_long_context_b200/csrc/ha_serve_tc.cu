@@ -1,0 +1,986 @@
+// ha_serve_tc.cu -- exact softmax attention for serving on the tensor cores (tcgen05 / TMEM / TMA), bf16 inputs: packed
+// prompts (causal, grouped heads) and trees of drafted tokens over a paged cache.
+//
+// A query tile has 128 rows: the query tokens of one key head times the heads that share it (row = token * group + head),
+// so every key tile that is loaded serves all of them. A work item has two tiles t = 0, 1, each with a softmax warpgroup of
+// its own, so that the tensor core multiplies for one while the other's exponentials run:
+//   PAIR: two neighbouring query tiles over the same key tiles (prompts; drafts of more than one tile);
+//   ALT:  one query tile, tile t takes every other key tile; the two results are joined in the epilogue (decoding and
+//         small trees, which are bound by reading the cache).
+// Tree items come from an even cut of all key tiles over the blocks (TreeWalk); pieces of a cut segment go to the
+// workspace and a second kernel joins them.
+//
+// Per unit (tile t, key tile): S = Q K^T (128 x 128, fp32, TMEM), P = 2^(c S - m) in bf16 over the first half of S's
+// columns, O_t += P V (TMEM). A thread of the softmax owns a query row; it keeps m and l in fp32 and rescales O only when
+// the maximum grows by more than 2^8 (P stays below 2^8; the sums are fp32, so the unscaled start costs no precision).
+// P is rounded to bf16 because the tensor core multiplies bf16; l sums the unrounded values.
+//
+// Issue order: S(next unit) goes out before P V(unit) is waited for when it belongs to the other tile, so a tile's P V and
+// next S run back to back while the other tile is in its softmax. A commit after S(j + 1) covers P V(j) too (same issuing
+// thread): a softmax thread that sees S(j + 1) may rescale O.
+//
+// Values of masked keys may be infinities or NaN: 0 * inf would reach rows that do not see them. Two warps look each
+// value tile over that some row does not see in full, replace what is not finite by 0 before the product and note it
+// for the item; the epilogue of a noted item adds those values to the rows that do see them.
+//
+// Block (384 threads, one per SM, persistent): warp 0 fetches the items and loads (TMA), warp 1 issues the MMAs, warps 2
+// and 3 look values over, warps 4-7 and 8-11 are the softmax of tile 0 and 1. Every wait is bounded; on expiry the status
+// word is set, all roles stop, the loader waits for its copies and TMEM is freed.
+#include <cuda.h>
+#include <math.h>
+
+#include "ha_common.cuh"
+#include "ha_internal.h"
+#include "ha_serve.cuh"
+#include "ha_sm100.cuh"
+
+namespace ha {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 384;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.0f;
+
+enum { PROMPT = 0, TREE_PAIR = 1, TREE_ALT = 2 };
+
+// One work item, published by the loader.
+struct Item {
+    int start, tok0, tokens, len;   // first query row, first token of tile 0 and query tokens of the sequence, keys in front
+    int kh, k0, n0, n1;             // key head, first key tile, key tiles of tile 0 and 1
+    int masked;                     // first key tile that some row does not see in full
+    int slot;                       // workspace slot of a piece, -1: the item is a whole segment
+    int last;                       // no item: the end
+    int odd;                        // a value that is not finite was replaced
+    int64_t kv;                     // tree: row of the page table; prompt: first key row
+    int k1;
+    int pad;
+};
+static_assert(sizeof(Item) == 64, "one item per 64 bytes");
+
+constexpr int kItems = 4;
+
+template <int D, int MODE>
+struct Cfg {
+    static constexpr bool ALT = MODE == TREE_ALT;
+    static constexpr int kTile = 128 * D * 2;      // 128 rows of bf16
+    static constexpr int NQ = ALT ? 1 : 2;
+    static constexpr int NK = D == 64 ? 6 : 3;
+    static constexpr int NV = D == 64 ? (ALT ? 6 : 5) : (ALT ? 3 : 2);
+    static constexpr int kQ = 0;
+    static constexpr int kK = NQ * kTile;
+    static constexpr int kV = kK + NK * kTile;
+    static constexpr int kItemsAt = kV + NV * kTile;
+    static constexpr int kStat = kItemsAt + kItems * 64;           // ALT: maximum and sum of tile 1's rows
+    static constexpr int kBars = kStat + (ALT ? 128 * 8 : 0);
+    static constexpr int bQFull = 0, bQEmpty = bQFull + 2, bKFull = bQEmpty + 2, bKEmpty = bKFull + NK,
+                         bVFull = bKEmpty + NK, bVOk = bVFull + NV, bVEmpty = bVOk + NV, bItemFull = bVEmpty + NV,
+                         bItemEmpty = bItemFull + kItems, bSFull = bItemEmpty + kItems, bPFull = bSFull + 2,
+                         bODone = bPFull + 2, bOFree = bODone + 2, bStat = bOFree + 2, bDrain = bStat + 1,
+                         kNumBars = bDrain + 1;
+    static constexpr int kTmemSlot = kBars + kNumBars * 8;
+    static constexpr int kAbort = kTmemSlot + 4;
+    static constexpr int kBytes = kAbort + 4 + 1024;               // and room to align the base to 1024
+    static_assert(kBars % 8 == 0, "mbarriers need 8-byte alignment");
+    static_assert(kBytes <= 232448, "shared memory budget");
+};
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+struct TcArgs {
+    ServeArgs a;
+    int tpt;         // query tokens of a tile
+    int box_rows;    // rows that a Q load brings
+    int plan;        // prompt: items come from the list in the workspace
+};
+
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
+                     "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::
+                     "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// ---------------------------------------------------------------------------------------------- prompt items
+//
+// The items of a prompt call (sequence, pair of query tiles) cost as many key tiles as lie in front of them. With many
+// sequences a one-block kernel lists them by falling position, so that the persistent blocks, which take them in turn
+// (to and fro), end together; with one sequence the list is known.
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanBuckets = 4096;
+
+struct PromptPlan {
+    int count;
+    int pad[3];
+};
+
+__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const ServeArgs a, int pair_tokens, int capacity) {
+    __shared__ int cursor[kPlanBuckets];
+    __shared__ int sums[32];
+    PromptPlan *head = static_cast<PromptPlan *>(a.ws);
+    int2 *list = reinterpret_cast<int2 *>(head + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int levels = (a.max_len + pair_tokens - 1) / pair_tokens;
+    int shift = 0;
+    while ((levels - 1) >> shift >= kPlanBuckets) ++shift;
+    const int buckets = ((levels - 1) >> shift) + 1;
+    for (int b = tid; b < buckets; b += kPlanThreads) cursor[b] = 0;
+    __syncthreads();
+    bool ok = true;
+    for (int s = warp; s < a.seqs; s += 32) {
+        int start, len;
+        ok &= prompt_seq(a, s, &start, &len);
+        const int pairs = (len + pair_tokens - 1) / pair_tokens;
+        for (int p = lane; p < pairs; p += 32) atomicAdd(&cursor[buckets - 1 - (p >> shift)], 1);
+    }
+    if (!ok && lane == 0) atomicOr(a.status, kStatusData);
+    __syncthreads();
+    // exclusive sums over the buckets, highest position first: four buckets per thread
+    int mine[kPlanBuckets / kPlanThreads], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanBuckets / kPlanThreads; ++i) {
+        const int b = tid * (kPlanBuckets / kPlanThreads) + i;
+        mine[i] = sum;
+        sum += b < buckets ? cursor[b] : 0;
+    }
+    int x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int w = sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        sums[lane] = w;
+    }
+    __syncthreads();
+    const int before = x - sum + (warp ? sums[warp - 1] : 0);
+#pragma unroll
+    for (int i = 0; i < kPlanBuckets / kPlanThreads; ++i) {
+        const int b = tid * (kPlanBuckets / kPlanThreads) + i;
+        if (b < buckets) cursor[b] = before + mine[i];
+    }
+    if (tid == 0) head->count = min(sums[31], capacity);   // overlapping sequences (reported) could ask for more
+    __syncthreads();
+    for (int s = warp; s < a.seqs; s += 32) {
+        int start, len;
+        prompt_seq(a, s, &start, &len);
+        const int pairs = (len + pair_tokens - 1) / pair_tokens;
+        for (int p = lane; p < pairs; p += 32) {
+            const int at = atomicAdd(&cursor[buckets - 1 - (p >> shift)], 1);
+            if (at < capacity) list[at] = make_int2(s, p);
+        }
+    }
+}
+
+// The block's own copy of the walk over a prompt call's items: (sequence, pair) of item i.
+struct PromptWalk {
+    int64_t count;    // items times key heads
+    int64_t round;
+    // One sequence, or few enough items for one round of blocks: no list.
+    __device__ __forceinline__ void begin(const TcArgs &x) {
+        const ServeArgs &a = x.a;
+        const int lane = threadIdx.x & 31;
+        round = 0;
+        if (x.plan) {
+            count = static_cast<int64_t>(static_cast<const PromptPlan *>(a.ws)->count) * a.kv_heads;
+            return;
+        }
+        int64_t pairs = 0;
+        bool ok = true;
+        for (int b = 0; b < a.seqs; b += 32) {
+            int start = 0, len = 0;
+            if (b + lane < a.seqs) ok &= prompt_seq(a, b + lane, &start, &len);
+            pairs += (len + 2 * x.tpt - 1) / (2 * x.tpt);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
+        if (!ok && blockIdx.x == 0) atomicOr(a.status, kStatusData);
+        count = pairs * a.kv_heads;
+    }
+    __device__ __forceinline__ bool next(const TcArgs &x, int *seq, int *pair, int *kh) {
+        const ServeArgs &a = x.a;
+        const int lane = threadIdx.x & 31;
+        const int64_t turn = (round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+        const int64_t i = round * gridDim.x + turn;
+        ++round;
+        if (i >= count) return false;   // the last round is not full
+        *kh = static_cast<int>(i % a.kv_heads);
+        const int64_t at = i / a.kv_heads;
+        if (x.plan) {
+            const int2 e = reinterpret_cast<const int2 *>(static_cast<const PromptPlan *>(a.ws) + 1)[at];
+            *seq = e.x;
+            *pair = e.y;
+            return true;
+        }
+        int64_t run = 0;
+        for (int b = 0; b < a.seqs; b += 32) {
+            int start = 0, len = 0;
+            if (b + lane < a.seqs) prompt_seq(a, b + lane, &start, &len);
+            const int64_t mine = (len + 2 * x.tpt - 1) / (2 * x.tpt);
+            int64_t sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t z = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += z;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, run + sum > at);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                *seq = b + l;
+                const int64_t pairs = __shfl_sync(0xffffffffu, mine, l);
+                *pair = static_cast<int>(pairs - 1 - (at - run - __shfl_sync(0xffffffffu, sum - mine, l)));
+                return true;
+            }
+            run += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        return false;
+    }
+};
+
+// ---------------------------------------------------------------------------------------------- masks
+
+// Which of the 32 keys from `first` on (relative to the tile's keys) a row sees.
+// prompt: the keys up to `own`; tree: the committed keys and the drafted ones set in bits.
+__device__ __forceinline__ uint32_t seen_causal(int own, int first) {
+    const int n = own + 1 - first;
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+__device__ __forceinline__ uint32_t seen_tree(uint64_t bits, int len, int first) {
+    const int s = first - len;   // drafted row of the first key
+    if (s <= -32) return 0xffffffffu;
+    if (s >= 64) return 0u;
+    if (s >= 0) return static_cast<uint32_t>(bits >> s);
+    return static_cast<uint32_t>(bits << -s) | ((1u << -s) - 1u);
+}
+
+// ---------------------------------------------------------------------------------------------- the kernel
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, const __grid_constant__ Maps maps) {
+    using C = Cfg<D, MODE>;
+    constexpr bool ALT = C::ALT, TREE = MODE != PROMPT;
+    const ServeArgs &a = x.a;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+    unsigned char *sm = smem_raw + pad;
+    const uint32_t sbase = raw_addr + pad;
+    auto bar = [&](int i) -> uint32_t { return sbase + C::kBars + 8u * static_cast<uint32_t>(i); };
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::kAbort);
+    Item *items = reinterpret_cast<Item *>(sm + C::kItemsAt);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(C::bQFull + i), 1);
+            mbar_init(bar(C::bQEmpty + i), 1);
+            mbar_init(bar(C::bSFull + i), 1);
+            mbar_init(bar(C::bPFull + i), 128);
+            mbar_init(bar(C::bODone + i), 1);
+            mbar_init(bar(C::bOFree + i), 128);
+        }
+        for (int i = 0; i < C::NK; ++i) {
+            mbar_init(bar(C::bKFull + i), 1);
+            mbar_init(bar(C::bKEmpty + i), 1);
+        }
+        for (int i = 0; i < C::NV; ++i) {
+            mbar_init(bar(C::bVFull + i), 1);
+            mbar_init(bar(C::bVOk + i), 64);
+            mbar_init(bar(C::bVEmpty + i), 1);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(bar(C::bItemFull + i), 1);
+            mbar_init(bar(C::bItemEmpty + i), 11);   // MMA issuer, two looking warps, eight softmax warps
+        }
+        mbar_init(bar(C::bStat), 128);
+        mbar_init(bar(C::bDrain), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_map(&maps.q);
+            prefetch_map(&maps.k);
+            prefetch_map(&maps.v);
+        }
+        tmem_alloc(sbase + C::kTmemSlot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + C::kTmemSlot);
+    grid_dependency_wait();   // the list of prompt items, if a kernel in front of this one makes it
+
+    // a wait of a whole warp: all of its lanes go on or none
+    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag)); };
+    // the item ring, read by all roles but the loader
+    auto item_bar = [&](uint32_t i) -> uint32_t { return bar(C::bItemFull + i % kItems); };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ items and loads
+        bool ok = true;
+        uint32_t ni = 0, nk = 0, nv = 0, nq[2] = {0, 0};   // items published, loads issued
+        PromptWalk pw;
+        TreeWalk tw;
+        const int tok_tile = ALT ? x.tpt : 2 * x.tpt;
+        if (TREE) {
+            tw.begin(a, 128, 0, tok_tile, blockIdx.x, gridDim.x);
+            if (lane == 0) tree_joins(a.ws)[blockIdx.x].pieces = 0;
+        } else {
+            pw.begin(x);
+        }
+        const int page = 1 << a.page_shift, per_tile = page >= 128 ? 1 : 128 >> a.page_shift;
+        for (;;) {
+            Item it{};
+            TreePiece p;
+            bool got;
+            if (TREE) {
+                got = tw.next(a, 128, 0, tok_tile, &p);
+                if (got) {
+                    it.start = p.x.start;
+                    it.tok0 = p.tile * tok_tile;
+                    it.tokens = p.x.t;
+                    it.len = p.x.len;
+                    it.kh = p.kh;
+                    it.k0 = p.k0;
+                    it.k1 = p.k1;
+                    it.masked = p.x.len >> 7;
+                    it.slot = p.k0 == 0 && p.k1 == p.nk ? -1 : 2 * static_cast<int>(blockIdx.x) + (p.k0 == 0);
+                    it.kv = p.x.table;
+                    const int n = p.k1 - p.k0;
+                    it.n0 = ALT ? (n + 1) >> 1 : n;
+                    it.n1 = ALT ? n >> 1 : it.tok0 + x.tpt < it.tokens ? n : 0;
+                    if (p.k0 == 0 && it.slot >= 0 && lane == 0) {
+                        TreeJoin j{};
+                        j.pieces = tree_pieces(p, blockIdx.x);
+                        j.start = it.start;
+                        j.row0 = it.tok0 * a.group;
+                        j.rows = min(tok_tile, it.tokens - it.tok0) * a.group;
+                        j.kh = it.kh;
+                        tree_joins(a.ws)[blockIdx.x] = j;
+                    }
+                }
+            } else {
+                int seq, pair, kh;
+                got = pw.next(x, &seq, &pair, &kh);
+                if (got) {
+                    prompt_seq(a, seq, &it.start, &it.tokens);
+                    it.tok0 = pair * 2 * x.tpt;
+                    it.kh = kh;
+                    it.masked = (it.tok0 + 1) >> 7;
+                    it.slot = -1;
+                    it.kv = it.start;
+                    it.n0 = (min(it.tokens, it.tok0 + x.tpt) + 127) >> 7;
+                    it.n1 = it.tok0 + x.tpt < it.tokens ? (min(it.tokens, it.tok0 + 2 * x.tpt) + 127) >> 7 : 0;
+                    it.k1 = max(it.n0, it.n1);
+                }
+            }
+            it.last = !got;
+            const int is = ni % kItems;
+            if (ni >= kItems && !warp_wait(bar(C::bItemEmpty + is), (ni / kItems - 1) & 1)) { ok = false; break; }
+            if (lane == 0) {
+                items[is] = it;
+                mbar_arrive(bar(C::bItemFull + is));
+            }
+            __syncwarp();
+            ++ni;
+            if (!got) break;
+            const int n = it.k1 - it.k0;
+            const int keys = it.len + it.tokens;
+            // page of this lane's part of key tile j (tree), -1 where the load is to bring zeros
+            auto page_of = [&](int kt) -> int {
+                int id = -1;
+                if (TREE && lane < per_tile) {
+                    const int first = page >= 128 ? kt * 128 : kt * 128 + lane * page;
+                    if (first < keys) {
+                        id = a.table[it.kv + (first >> a.page_shift)];
+                        if (id < 0 || id >= a.pages) {
+                            atomicOr(a.status, kStatusData);
+                            id = -1;
+                        }
+                    }
+                }
+                return id;
+            };
+            auto load_tile = [&](const CUtensorMap *map, uint32_t dst, uint32_t b, int kt, int id) {
+                if (lane == 0) mbar_arrive_expect_tx(b, C::kTile);
+                __syncwarp();
+                if (TREE) {
+                    if (lane < per_tile) {
+                        const int z = id < 0 ? static_cast<int>(a.pages) : id;   // past the last page: zeros
+                        const int y = page > 128 ? (kt * 128) & (page - 1) : 0;
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_4d(dst + h * 16384 + lane * (page << 7), map, b, h * 64, y, it.kh, z);
+                    }
+                } else if (lane == 0) {
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h) tma_3d(dst + h * 16384, map, b, h * 64, it.kh, static_cast<int>(it.kv) + kt * 128);
+                }
+            };
+            auto load_k = [&](int kt, int id) -> bool {
+                const int s = nk % C::NK;
+                if (nk >= C::NK && !warp_wait(bar(C::bKEmpty + s), (nk / C::NK - 1) & 1)) return false;
+                load_tile(&maps.k, sbase + C::kK + s * C::kTile, bar(C::bKFull + s), kt, id);
+                ++nk;
+                return true;
+            };
+            auto load_v = [&](int kt, int id) -> bool {
+                const int s = nv % C::NV;
+                if (nv >= C::NV && !warp_wait(bar(C::bVEmpty + s), (nv / C::NV - 1) & 1)) return false;
+                load_tile(&maps.v, sbase + C::kV + s * C::kTile, bar(C::bVFull + s), kt, id);
+                ++nv;
+                return true;
+            };
+            int id = page_of(it.k0), ahead = n > 1 ? page_of(it.k0 + 1) : -1;
+            ok = load_k(it.k0, id);
+            for (int t = 0; t < C::NQ && ok; ++t) {
+                if (!ALT && (t == 0 ? it.n0 : it.n1) == 0) continue;
+                if (nq[t] >= 1 && !warp_wait(bar(C::bQEmpty + t), (nq[t] - 1) & 1)) { ok = false; break; }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(C::bQFull + t), x.box_rows * D * 2);
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h)
+                        tma_3d(sbase + C::kQ + t * C::kTile + h * 16384, &maps.q, bar(C::bQFull + t), h * 64, it.kh * a.group,
+                               it.start + it.tok0 + t * x.tpt);
+                }
+                __syncwarp();
+                ++nq[t];
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                const int far = j + 2 < n ? page_of(it.k0 + j + 2) : -1;
+                if (j + 1 < n) ok = load_k(it.k0 + j + 1, ahead);
+                if (ok) ok = load_v(it.k0 + j, id);
+                id = ahead;
+                ahead = far;
+            }
+            if (!ok) break;
+        }
+        if (!ok) {
+            if (lane == 0) atomicOr(a.status, kStatusTimeout);
+            // the copies in flight land before the block ends
+            volatile int no_abort = 0;
+            for (uint32_t i = nk > C::NK ? nk - C::NK : 0; i < nk; ++i)
+                mbar_wait(bar(C::bKFull + i % C::NK), (i / C::NK) & 1, &no_abort, 200000000ull);
+            for (uint32_t i = nv > C::NV ? nv - C::NV : 0; i < nv; ++i)
+                mbar_wait(bar(C::bVFull + i % C::NV), (i / C::NV) & 1, &no_abort, 200000000ull);
+            for (int t = 0; t < C::NQ; ++t)
+                if (nq[t]) mbar_wait(bar(C::bQFull + t), (nq[t] - 1) & 1, &no_abort, 200000000ull);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false, false);
+            constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
+            const uint64_t dq0 = smem_desc(sbase + C::kQ, 16, 1024);
+            const uint64_t dk0 = smem_desc(sbase + C::kK, 16, 1024);
+            const uint64_t dv0 = smem_desc(sbase + C::kV, 16384, 1024);
+            bool ok = true;
+            struct Unit {
+                uint32_t item;       // number of the item
+                uint32_t base;       // number of the item's first key tile among the block's loads
+                int n0, n1, j, t;
+                bool end;
+            };
+            uint32_t cq[2] = {0, 0};   // items of tile t whose Q has been waited for (ALT: entry 0)
+            uint32_t cp[2] = {0, 0};   // P tiles consumed
+            uint32_t co[2] = {0, 0};   // items of tile t begun (P V)
+            auto tile_of = [&](const Unit &u) -> uint32_t { return u.base + (ALT ? 2 * u.j + u.t : u.j); };
+            auto first_of = [&](Unit &u) {      // first unit of item u.item (published)
+                const Item &it = items[u.item % kItems];
+                u.n0 = it.n0;
+                u.n1 = it.n1;
+                u.end = it.last != 0;
+                u.j = 0;
+                u.t = 0;                         // tile 0 always has keys
+            };
+            // the unit behind u; false if its item is not there yet and block is not set
+            auto advance = [&](const Unit &u, Unit &v, bool block) -> bool {
+                v = u;
+                const int most = max(u.n0, u.n1);
+                do {
+                    if (v.t == 0) v.t = 1;
+                    else { v.t = 0; ++v.j; }
+                } while (v.j < most && v.j >= (v.t == 0 ? v.n0 : v.n1));
+                if (v.j < most) return true;
+                v.item = u.item + 1;
+                v.base = u.base + (ALT ? u.n0 + u.n1 : most);
+                const uint32_t b = bar(C::bItemFull + v.item % kItems), par = (v.item / kItems) & 1;
+                if (block) {
+                    if (!mbar_wait(b, par, abort_flag)) { ok = false; return false; }
+                } else if (!mbar_try_wait(b, par)) {
+                    return false;
+                }
+                first_of(v);
+                return true;
+            };
+            auto issue_s = [&](const Unit &u, bool block) -> bool {
+                const uint32_t tile = tile_of(u);
+                const int s = tile % C::NK, qi = ALT ? 0 : u.t;
+                const bool new_q = u.j == 0 && (!ALT || u.t == 0);
+                const uint32_t kb = bar(C::bKFull + s), kpar = (tile / C::NK) & 1;
+                const uint32_t qb = bar(C::bQFull + qi), qpar = cq[qi] & 1;
+                if (block) {
+                    if (!mbar_wait(kb, kpar, abort_flag) || (new_q && !mbar_wait(qb, qpar, abort_flag))) { ok = false; return false; }
+                } else if (!mbar_try_wait(kb, kpar) || (new_q && !mbar_try_wait(qb, qpar))) {
+                    return false;
+                }
+                if (new_q) ++cq[qi];
+                tc_fence_after();
+                const uint64_t dq = dq0 + static_cast<uint64_t>((qi * C::kTile) >> 4);
+                const uint64_t dk = dk0 + static_cast<uint64_t>((s * C::kTile) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+                    mma_ss(tmem + u.t * 128, dq + off, dk + off, idesc_qk, kk > 0 ? 1u : 0u);
+                }
+                mma_commit(bar(C::bSFull + u.t));
+                const bool last_user = ALT || u.t == 1 || u.j >= u.n1;
+                if (last_user) mma_commit(bar(C::bKEmpty + s));
+                // the item's last score product with this Q
+                const bool last_q = !ALT ? u.j == (u.t == 0 ? u.n0 : u.n1) - 1
+                                         : u.t == 0 ? u.n0 == u.j + 1 && u.n1 <= u.j : u.n0 <= u.j + 1;
+                if (last_q) mma_commit(bar(C::bQEmpty + qi));
+                return true;
+            };
+            auto issue_pv = [&](const Unit &u) -> bool {
+                const uint32_t tile = tile_of(u);
+                const int s = tile % C::NV;
+                if (!mbar_wait(bar(C::bPFull + u.t), cp[u.t] & 1, abort_flag)) return false;
+                ++cp[u.t];
+                if (!mbar_wait(bar(C::bVOk + s), (tile / C::NV) & 1, abort_flag)) return false;
+                if (u.j == 0) {
+                    if (co[u.t] > 0 && !mbar_wait(bar(C::bOFree + u.t), (co[u.t] - 1) & 1, abort_flag)) return false;
+                    ++co[u.t];
+                }
+                tc_fence_after();
+                const uint64_t dv = dv0 + static_cast<uint64_t>((s * C::kTile) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ts(tmem + 256 + u.t * D, tmem + u.t * 128 + kk * 8, dv + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
+                           (u.j > 0 || kk > 0) ? 1u : 0u);
+                if (ALT || u.t == 1 || u.j >= u.n1) mma_commit(bar(C::bVEmpty + s));
+                if (u.j == (u.t == 0 ? u.n0 : u.n1) - 1) mma_commit(bar(C::bODone + u.t));
+                return true;
+            };
+            Unit cur{}, nxt{};
+            ok = mbar_wait(item_bar(0), 0, abort_flag);
+            if (ok) {
+                first_of(cur);
+                if (!cur.end) ok = issue_s(cur, true);
+            }
+            while (ok && !cur.end) {
+                bool known = advance(cur, nxt, false), issued = false;
+                if (known && !nxt.end && nxt.t != cur.t) issued = issue_s(nxt, false);
+                if (!issue_pv(cur)) { ok = false; break; }
+                if (!known && !advance(cur, nxt, true)) break;
+                if (nxt.item != cur.item) mbar_arrive(bar(C::bItemEmpty + cur.item % kItems));
+                if (!nxt.end && !issued && !issue_s(nxt, true)) break;
+                cur = nxt;
+            }
+            if (!ok) atomicOr(a.status, kStatusTimeout);
+            mma_commit(bar(C::bDrain));   // every MMA issued so far completes before TMEM is released
+            volatile int no_abort = 0;
+            mbar_wait(bar(C::bDrain), 0, &no_abort, 200000000ull);
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // ------------------------------------------------------------------ values of masked keys
+        bool ok = true;
+        uint32_t nv = 0;
+        for (uint32_t i = 0; ok; ++i) {
+            if (!warp_wait(item_bar(i), (i / kItems) & 1)) { ok = false; break; }
+            Item *it = &items[i % kItems];
+            if (it->last) break;
+            const int n = it->k1 - it->k0;
+            for (int j = 0; j < n; ++j, ++nv) {
+                const int s = nv % C::NV;
+                if (!warp_wait(bar(C::bVFull + s), (nv / C::NV) & 1)) { ok = false; break; }
+                if (it->k0 + j >= it->masked) {
+                    uint4 *tile = reinterpret_cast<uint4 *>(sm + C::kV + s * C::kTile);
+                    bool odd = false;
+#pragma unroll 4
+                    for (int e = (warp - 2) * 32 + lane; e < C::kTile / 16; e += 64) {
+                        uint4 w = tile[e];
+                        // an exponent of ones in either half carries into the bit above it
+                        auto bad = [](uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                        if (bad(w.x) | bad(w.y) | bad(w.z) | bad(w.w)) {
+                            auto clean = [&](uint32_t u) {
+                                const uint32_t b = bad(u);
+                                return u & ~((b & 0x80000000u ? 0xffff0000u : 0u) | (b & 0x8000u ? 0xffffu : 0u));
+                            };
+                            w.x = clean(w.x);
+                            w.y = clean(w.y);
+                            w.z = clean(w.z);
+                            w.w = clean(w.w);
+                            tile[e] = w;
+                            odd = true;
+                        }
+                    }
+                    if (odd) it->odd = 1;
+                    fence_proxy_async_smem();
+                }
+                mbar_arrive(bar(C::bVOk + s));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::bItemEmpty + i % kItems));
+        }
+    } else {
+        // ------------------------------------------------------------------ softmax and epilogue
+        const int t = (warp - 4) >> 2, q = warp & 3, r = q * 32 + lane;
+        const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        const uint32_t tS = trow + t * 128, tO = trow + 256 + t * D;
+        const float c = a.scale * kLog2e;
+        const uint64_t c2 = f2_pack(c, c);
+        const int my_tok = r / a.group, my_head = r - my_tok * a.group;   // within the tile
+        float2 *stat = reinterpret_cast<float2 *>(sm + C::kStat);
+        uint32_t ns = 0, no = 0, no1 = 0;   // score tiles read, items finished (and of tile 1, seen from tile 0: ALT)
+        bool ok = true;
+        for (uint32_t i = 0; ok; ++i) {
+            if (!warp_wait(item_bar(i), (i / kItems) & 1)) { ok = false; break; }
+            const volatile Item *it = &items[i % kItems];
+            if (it->last) break;
+            const int n = t == 0 ? it->n0 : it->n1, n1 = it->n1;
+            const int tok0 = it->tok0 + (ALT ? 0 : t * x.tpt);
+            const int rows = min(x.tpt, it->tokens - tok0) * a.group;
+            const bool mine = r < rows;
+            const bool active = q * 32 < rows;      // some row of the warp
+            const int tok = mine ? tok0 + my_tok : tok0;
+            const int k0 = it->k0, masked = TREE ? it->masked : (tok0 + 1) >> 7, len = it->len;
+            const uint64_t bits = TREE ? tree_bits(a, it->start, tok, it->tokens) : 0;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < n; ++j) {
+                if (!warp_wait(bar(C::bSFull + t), ns & 1)) { ok = false; break; }
+                ++ns;
+                tc_fence_after();
+                if (active) {
+                    const int kt = k0 + (ALT ? 2 * j + t : j);
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) tmem_ld32(tS + h * 32, s[h]);
+                    tmem_ld_wait();
+                    if (kt >= masked) {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const int first = kt * 128 + h * 32;
+                            const uint32_t seen = TREE ? seen_tree(bits, len, first) : seen_causal(tok, first);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(seen >> e & 1u)) s[h][e] = 0xff800000u;
+                        }
+                    }
+                    float top[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        top[h] = fmaxf(__uint_as_float(s[h][0]), __uint_as_float(s[h][1]));
+#pragma unroll
+                        for (int e = 2; e < 32; e += 2)
+                            top[h] = fmax3(top[h], __uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]));
+                    }
+                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+                    const bool grow = mx > m + kGrow;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float to = grow ? mx : m;
+                        const float alpha = grow ? ex2_approx(m - to) : 1.0f;
+                        l *= alpha;
+                        m = to;
+                        if (j > 0) {   // P V of the tiles before is complete: S of this one came behind it
+#pragma unroll
+                            for (int h = 0; h < D / 16; ++h) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + h * 16, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st16(tO + h * 16, o);
+                            }
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    const uint64_t off = f2_pack(-ref, -ref);
+                    uint64_t sum = f2_pack(0.f, 0.f), sum2 = sum;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[h][2 * e]), __uint_as_float(s[h][2 * e + 1])), c2, off));
+                            const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+                            if (e & 1) sum = f2_add(sum, f2_pack(p0, p1));
+                            else sum2 = f2_add(sum2, f2_pack(p0, p1));
+                            pk[e] = pack_bf16x2(p0, p1);
+                        }
+                        tmem_st16(tS + h * 16, pk);
+                    }
+                    const float2 both = f2_unpack(f2_add(sum, sum2));
+                    l += both.x + both.y;
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                mbar_arrive(bar(C::bPFull + t));
+            }
+            if (!ok) break;
+            // ---- epilogue
+            float w0 = 1.f, w1 = 0.f;
+            if (ALT && t == 1) {
+                if (n > 0) {
+                    // this item's first P V waited until tile 0 had read the previous item's O and statistics
+                    if (!warp_wait(bar(C::bODone + 1), no & 1)) { ok = false; break; }
+                    ++no;
+                    stat[r] = make_float2(m, l);
+                    mbar_arrive(bar(C::bStat));
+                }
+            } else if (n > 0) {
+                if (!warp_wait(bar(C::bODone + t), no & 1)) { ok = false; break; }
+                ++no;
+                if (ALT && n1 > 0) {
+                    if (!warp_wait(bar(C::bStat), no1 & 1) || !warp_wait(bar(C::bODone + 1), no1 & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    ++no1;
+                    const float2 other = stat[r];
+                    const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
+                    w0 = ex2_approx(m - ref);
+                    w1 = ex2_approx(other.x - ref);
+                    l = w0 * l + w1 * other.y;
+                    m = top;
+                }
+                tc_fence_after();
+                const int slot = it->slot;
+                const bool odd = it->odd != 0;
+                const bool join = ALT && n1 > 0;
+                const int head = it->kh * a.group + my_head;
+                const int64_t row = it->start + tok;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                float *part = nullptr;
+                if (TREE && slot >= 0)
+                    part = tree_slot(a.ws, gridDim.x, slot, ALT ? 128 : 256, D);
+                const int prow = r + (ALT ? 0 : t * x.tpt * a.group);   // row within the segment
+                if (active) {
+#pragma unroll 1
+                    for (int h = 0; h < D / 32; ++h) {
+                        __syncwarp();
+                        uint32_t o[32];
+                        tmem_ld32(tO + h * 32, o);
+                        tmem_ld_wait();
+                        if (join) {
+                            uint32_t o1[32];
+                            tmem_ld32(trow + 256 + D + h * 32, o1);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(w0 * __uint_as_float(o[e]) + w1 * __uint_as_float(o1[e]));
+                        }
+                        if (odd && mine) {
+                            // values that were replaced by 0: the rows that see them get them now
+                            const int end = min(it->len + it->tokens, it->k1 * 128);
+                            for (int key = max(it->masked, it->k0) * 128; key < end; ++key) {
+                                const bool sees = TREE ? seen_tree(bits, len, key) & 1u : key <= tok;
+                                if (!sees) continue;
+                                const uint16_t *v;
+                                if (TREE) {
+                                    const int id = a.table[it->kv + (key >> a.page_shift)];
+                                    if (id < 0 || id >= a.pages) continue;
+                                    v = static_cast<const uint16_t *>(a.vp) +
+                                        (((static_cast<int64_t>(id) * a.kv_heads + it->kh) << a.page_shift) +
+                                         (key & ((1 << a.page_shift) - 1))) * D;
+                                } else {
+                                    v = static_cast<const uint16_t *>(a.v) + (it->kv + key) * a.v_tok + it->kh * a.v_head;
+                                }
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const float f = bf16_bits_to_float(v[h * 32 + e]);
+                                    if (!(fabsf(f) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
+                                }
+                            }
+                        }
+                        if (!mine) continue;
+                        if (TREE && part) {
+                            float4 *dst = reinterpret_cast<float4 *>(part + prow * D + h * 32);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                     __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                            continue;
+                        }
+                        const int64_t at = row * a.o_tok + static_cast<int64_t>(head) * a.o_head + h * 32;
+                        if (a.out_dtype == 0) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int f = 0; f < 4; ++f)
+                                    w[f] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[8 * e + 2 * f]) * inv,
+                                                                       __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
+                                dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float w[4];
+#pragma unroll
+                                for (int f = 0; f < 4; ++f) w[f] = l == 0.f ? 0.f : __uint_as_float(o[4 * e + f]) * inv;
+                                dst[e] = make_float4(w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                    }
+                    if (mine) {
+                        if (TREE && part) {
+                            const int pr = ALT ? 128 : 256;
+                            part[pr * D + prow] = m;
+                            part[pr * (D + 1) + prow] = l;
+                        } else if (a.lse) {
+                            a.lse[static_cast<int64_t>(head) * a.tokens + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                        }
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(bar(C::bOFree + t));
+                if (join) mbar_arrive(bar(C::bOFree + 1));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::bItemEmpty + i % kItems));
+        }
+        if (!ok) atomicOr(a.status, kStatusTimeout);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------- host
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+    static const EncodeFn fn = []() -> EncodeFn {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// A bf16 tensor map with boxes of 64 columns (128 bytes, 128-byte swizzle). stride: elements of dimensions 1 .. rank-1.
+bool make_map(CUtensorMap *map, const void *base, int rank, const int64_t *dims, const int64_t *strides, const int *box) {
+    const EncodeFn fn = encoder();
+    if (!fn) return false;
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], e[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = static_cast<cuuint64_t>(dims[i]);
+        b[i] = static_cast<cuuint32_t>(box[i]);
+        e[i] = 1;
+        if (i) s[i - 1] = static_cast<cuuint64_t>(strides[i - 1]) * 2;
+    }
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_rows_map(CUtensorMap *map, const void *base, int d, int heads, int64_t tokens, int64_t head, int64_t token, int box_heads,
+                   int box_tokens) {
+    const int64_t dims[3] = {d, heads, tokens}, strides[2] = {head, token};
+    const int box[3] = {64, box_heads, box_tokens};
+    return make_map(map, base, 3, dims, strides, box);
+}
+
+template <int D, int MODE>
+bool launch(const TcArgs &x, const Maps &maps, int blocks, bool dependent, cudaStream_t st) {
+    using C = Cfg<D, MODE>;
+    if (cudaFuncSetAttribute(serve_tc_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes) != cudaSuccess)
+        return false;
+    if (dependent) return launch_dependent(serve_tc_kernel<D, MODE>, dim3(blocks), dim3(kThreads), C::kBytes, st, x, maps);
+    serve_tc_kernel<D, MODE><<<blocks, kThreads, C::kBytes, st>>>(x, maps);
+    return cudaPeekAtLastError() == cudaSuccess;
+}
+
+// Items of a prompt call: every sequence has at most one pair of tiles that is not full.
+int64_t prompt_items(int64_t tokens, int64_t seqs, int tpt) { return tokens / (2 * tpt) + seqs; }
+
+}  // namespace
+
+size_t serve_prompt_workspace(int64_t tokens, int64_t seqs, int group) {
+    if (group > 128) return 0;
+    return sizeof(PromptPlan) + static_cast<size_t>(prompt_items(tokens, seqs, 128 / group)) * sizeof(int2);
+}
+
+int launch_prompt_tc(const ServeArgs &a, cudaStream_t st) {
+    TcArgs x{};
+    x.a = a;
+    x.tpt = 128 / a.group;
+    const int box_tokens = static_cast<int>(a.max_len < x.tpt ? a.max_len : x.tpt);
+    x.box_rows = box_tokens * a.group;
+    const int64_t items = prompt_items(a.tokens, a.seqs, x.tpt);
+    if (items > 0x7fffffff) return -2;
+    x.plan = a.seqs > 1 && items * a.kv_heads > a.sms;
+    Maps maps;
+    if (!make_rows_map(&maps.q, a.q, a.d, a.heads, a.tokens, a.q_head, a.q_tok, a.group, box_tokens) ||
+        !make_rows_map(&maps.k, a.k, a.d, a.kv_heads, a.tokens, a.k_head, a.k_tok, 1, 128) ||
+        !make_rows_map(&maps.v, a.v, a.d, a.kv_heads, a.tokens, a.v_head, a.v_tok, 1, 128))
+        return -2;
+    if (x.plan) {
+        prompt_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, 2 * x.tpt, static_cast<int>(items));
+        if (cudaPeekAtLastError() != cudaSuccess) return -1;
+    }
+    const int64_t most = items * a.kv_heads;
+    const int blocks = static_cast<int>(most < a.sms ? most : a.sms);
+    const bool ok = a.d == 64 ? launch<64, PROMPT>(x, maps, blocks, x.plan, st) : launch<128, PROMPT>(x, maps, blocks, x.plan, st);
+    return ok ? 1 + x.plan : -1;
+}
+
+int launch_tree_tc(const ServeArgs &a, cudaStream_t st) {
+    TcArgs x{};
+    x.a = a;
+    x.tpt = 128 / a.group;
+    const int box_tokens = a.max_len < x.tpt ? a.max_len : x.tpt;
+    x.box_rows = box_tokens * a.group;
+    const bool alt = a.max_len <= x.tpt;
+    const int page = 1 << a.page_shift;
+    Maps maps;
+    const int64_t dims[4] = {a.d, page, a.kv_heads, a.pages};
+    const int64_t strides[3] = {a.d, static_cast<int64_t>(a.d) * page, static_cast<int64_t>(a.d) * page * a.kv_heads};
+    const int box[4] = {64, page < 128 ? page : 128, 1, 1};
+    if (!make_rows_map(&maps.q, a.q, a.d, a.heads, a.tokens, a.q_head, a.q_tok, a.group, box_tokens) ||
+        !make_map(&maps.k, a.kp, 4, dims, strides, box) || !make_map(&maps.v, a.vp, 4, dims, strides, box))
+        return -2;
+    bool ok;
+    if (alt) ok = a.d == 64 ? launch<64, TREE_ALT>(x, maps, a.sms, false, st) : launch<128, TREE_ALT>(x, maps, a.sms, false, st);
+    else ok = a.d == 64 ? launch<64, TREE_PAIR>(x, maps, a.sms, false, st) : launch<128, TREE_PAIR>(x, maps, a.sms, false, st);
+    if (!ok) return -1;
+    return launch_tree_join(a, a.sms, alt ? 128 : 256, st) ? 2 : -1;
+}
+
+}  // namespace ha
