@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -74,6 +75,9 @@ class CacheArgs(ctypes.Structure):
                 [(n, ctypes.c_int) for n in ("kv_heads", "page", "d")])
 
 
+_STRIDES = ctypes.c_int64 * 3
+
+
 class TreeArgs(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "o", "lse")] + [("tokens", ctypes.c_int64)] +
                 [(n, ctypes.c_int64) for n in ("q_token", "q_head", "o_token", "o_head")] +
@@ -120,7 +124,7 @@ def lib():
     L.hyper_attn_profile_read.argtypes = [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ci), ci]
     st = ctypes.c_size_t
     L.hyper_attn_prompt.argtypes = [vp, ctypes.POINTER(PromptArgs)]
-    L.hyper_attn_prompt_workspace.argtypes = [i64, i64, ci, ci]
+    L.hyper_attn_prompt_workspace.argtypes = [vp, i64, i64, ci, ci]
     L.hyper_attn_prompt_workspace.restype = st
     cache = ctypes.POINTER(CacheArgs)
     L.hyper_attn_tree.argtypes = [vp, cache, ctypes.POINTER(TreeArgs)]
@@ -131,9 +135,14 @@ def lib():
     L.hyper_attn_cache_workspace.argtypes = [i64, i64]
     L.hyper_attn_cache_workspace.restype = st
     L.hyper_attn_cache_reserve.argtypes = [vp, cache, vp, vp, i64, vp, vp, st]
-    strides = ctypes.POINTER(i64 * 3)
+    strides = ctypes.POINTER(ctypes.c_int64)
     L.hyper_attn_cache_append.argtypes = [vp, cache, vp, vp, i64, i64, vp, vp, strides, strides, i64, i64]
     L.hyper_attn_cache_commit.argtypes = [vp, cache, vp, vp, vp, i64, i64]
+    # the same entry points taking the argument struct as packed bytes
+    L.prompt_packed = L["hyper_attn_prompt"]
+    L.prompt_packed.argtypes = [vp, ctypes.c_char_p]
+    L.tree_packed = L["hyper_attn_tree"]
+    L.tree_packed.argtypes = [vp, cache, ctypes.c_char_p]
     _lib = L
     return L
 
@@ -181,12 +190,27 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _ints(t, device: int, what: str, count=None, bits=32):
-    """The address of a contiguous device tensor of integers."""
-    kind = str(t.dtype)
-    _need(kind == f"torch.int{bits}" and t.is_contiguous() and t.device.type == "cuda" and t.device.index == device,
-          f"{what}: a contiguous int{bits} tensor on the handle's device is needed")
-    _need(count is None or t.numel() == count, f"{what}: {count} values are needed, got {t.numel()}")
+# The argument structs of the serving calls are packed with `struct` (native alignment): filling a ctypes Structure field by
+# field takes several times as long, and these calls run once per layer and token.
+_PROMPT = struct.Struct("@5Pq8q3iPqqfPN")
+_TREE = struct.Struct("@3Pq4qiq3PqifPN")
+_torch = None
+
+
+def _import_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
+def _ints(t, device: int, what: str, count=None, wide=False):
+    """The address of a contiguous device tensor of int32 (wide: int64) values."""
+    torch = _torch or _import_torch()
+    if t.dtype is not (torch.int64 if wide else torch.int32) or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous int{64 if wide else 32} tensor on the handle's device is needed")
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{what}: {count} values are needed, got {t.numel()}")
     return t.data_ptr()
 
 
@@ -195,14 +219,18 @@ class PagedCache:
     table [slots, max_pages], lens and held [slots], refs [pages] (int32). The tensors stay the caller's."""
 
     def __init__(self, k, v, table, lens, held, refs):
-        _need(k.dim() == 5 and k.shape == v.shape and k.dtype == v.dtype, "k and v: [layers, pages, kv_heads, page, d] alike")
-        _need(k.is_contiguous() and v.is_contiguous(), "tensors must be contiguous")
-        _need(k.device.type == "cuda" and v.device == k.device, "the cache must be on one CUDA device")
-        layers, pages, kv_heads, page, d = k.shape
+        shape, device = k.shape, k.get_device()
+        if len(shape) != 5 or v.shape != shape or v.dtype is not k.dtype:
+            raise ValueError("k and v: [layers, pages, kv_heads, page, d] of one type are needed")
+        if not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("tensors must be contiguous")
+        if device < 0 or v.get_device() != device:
+            raise ValueError("the cache must be on one CUDA device")
+        layers, pages, kv_heads, page, d = shape
         slots, max_pages = table.shape
-        device = k.device.index
         self.k, self.v, self.table, self.lens, self.held, self.refs = k, v, table, lens, held, refs
-        self.device, self.dtype = device, str(k.dtype)
+        self.device, self.dtype = device, k.dtype
+        self.pages, self.kv_heads, self.page, self.d = pages, kv_heads, page, d
         self.args = CacheArgs(k.data_ptr(), v.data_ptr(), _ints(table, device, "table"), _ints(lens, device, "lens", slots),
                               _ints(held, device, "held", slots), _ints(refs, device, "refs", pages), layers, pages, slots,
                               max_pages, kv_heads, page, d)
@@ -210,7 +238,7 @@ class PagedCache:
     @classmethod
     def empty(cls, *, layers, pages, kv_heads, page, d, slots, max_pages, dtype="bf16", device=0):
         """A new cache with all pages free and all slots empty."""
-        import torch
+        torch = _torch or _import_torch()
         dev = torch.device("cuda", device)
         shape = (layers, pages, kv_heads, page, d)
         kind = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
@@ -229,6 +257,7 @@ class HyperAttention:
             raise HAError(rc, f"hyper_attn_create(device={device}) failed")
         self.options = default_options()
         self.device = device
+        self._device_object = None
 
     def _check(self, rc: int):
         if rc:
@@ -282,32 +311,44 @@ class HyperAttention:
     # ---- serving: exact attention over packed prompts and over a paged cache, and the cache's steps
 
     def _rows(self, t, what: str, dtype: int):
-        """[tokens, heads, d] device tensor of the given type, with a contiguous last dimension."""
-        _need(t.dim() == 3 and (t.shape[2] == 1 or t.stride(2) == 1), f"{what}: [tokens, heads, d] with contiguous rows is needed")
-        _need(str(t.dtype) == ("torch.bfloat16" if dtype == 0 else "torch.float32"),
-              f"{what}: the handle's options say {'bf16' if dtype == 0 else 'fp32'}, got {t.dtype}")
-        _need(t.device.type == "cuda" and t.device.index == self.device, f"{what}: on the handle's device")
-        return t.data_ptr(), t.stride(0), t.stride(1)
+        """Address and strides of a [tokens, heads, d] device tensor of the given type with a contiguous last dimension."""
+        torch = _torch or _import_torch()
+        stride = t.stride()
+        if len(stride) != 3 or (stride[2] != 1 and t.shape[2] != 1):
+            raise ValueError(f"{what}: [tokens, heads, d] with contiguous rows is needed")
+        if t.dtype is not (torch.float32 if dtype else torch.bfloat16):
+            raise ValueError(f"{what}: the handle's options say {'fp32' if dtype else 'bf16'}, got {t.dtype}")
+        if t.get_device() != self.device:
+            raise ValueError(f"{what}: on the handle's device")
+        return t.data_ptr(), stride[0], stride[1]
 
     def _workspace(self, nbytes: int):
         """A device buffer whose reuse is ordered by the handle's stream (a graph under capture gets its own)."""
-        import torch
+        if not nbytes:
+            return None
+        torch = _torch or _import_torch()
         stream = self.options.stream or 0
         if stream == torch.cuda.current_stream(self.device).cuda_stream:
-            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=torch.device("cuda", self.device))
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device) if stream
+            return torch.empty(nbytes, dtype=torch.uint8, device=self._torch_device())
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self._torch_device()) if stream
                                else torch.cuda.default_stream(self.device)):
-            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=torch.device("cuda", self.device))
+            return torch.empty(nbytes, dtype=torch.uint8, device=self._torch_device())
+
+    def _torch_device(self):
+        if self._device_object is None:
+            self._device_object = (_torch or _import_torch()).device("cuda", self.device)
+        return self._device_object
 
     def _out_dtype(self) -> int:
-        return self.options.dtype if self.options.out_dtype < 0 else self.options.out_dtype
+        out = self.options.out_dtype
+        return self.options.dtype if out < 0 else out
 
     def _lse(self, lse, heads: int, tokens: int):
         if lse is None:
             return None
-        _need(tuple(lse.shape) == (heads, tokens) and lse.is_contiguous() and str(lse.dtype) == "torch.float32" and
-              lse.device.type == "cuda" and lse.device.index == self.device,
-              "lse: contiguous fp32 [heads, tokens] on the handle's device is needed")
+        if (lse.shape != (heads, tokens) or lse.dtype is not _torch.float32 or lse.get_device() != self.device or
+                not lse.is_contiguous()):
+            raise ValueError("lse: contiguous fp32 [heads, tokens] on the handle's device is needed")
         return lse.data_ptr()
 
     def prompt(self, Q, K, V, O, offsets, *, max_len=None, scale=1.0, lse=None):
@@ -317,24 +358,29 @@ class HyperAttention:
         dt = self.options.dtype
         q, k, v = self._rows(Q, "Q", dt), self._rows(K, "K", dt), self._rows(V, "V", dt)
         o = self._rows(O, "O", self._out_dtype())
-        tokens, heads, d = Q.shape
-        kv_heads = K.shape[1]
-        _need(O.shape == Q.shape and K.shape == V.shape and K.shape[0] == tokens and K.shape[2] == d,
-              "Q, O [tokens, heads, d] and K, V [tokens, kv_heads, d] are needed")
-        _need(offsets.numel() >= 1, "offsets: at least one value is needed")
+        tokens, heads, d = shape = Q.shape
+        kshape = K.shape
+        kv_heads = kshape[1]
+        if O.shape != shape or V.shape != kshape or kshape[0] != tokens or kshape[2] != d:
+            raise ValueError("Q, O [tokens, heads, d] and K, V [tokens, kv_heads, d] are needed")
         at = _ints(offsets, self.device, "offsets")
         seqs = offsets.numel() - 1
-        ws = self._workspace(lib().hyper_attn_prompt_workspace(tokens, seqs, heads, kv_heads))
-        a = PromptArgs(q[0], k[0], v[0], o[0], self._lse(lse, heads, tokens), tokens, q[1], q[2], k[1], k[2], v[1], v[2],
-                       o[1], o[2], heads, kv_heads, d, at, seqs, max(tokens, 1) if max_len is None else max_len, scale,
-                       ws.data_ptr(), ws.numel())
-        self._check(lib().hyper_attn_prompt(self._h, ctypes.byref(a)))
+        L = _lib
+        nbytes = L.hyper_attn_prompt_workspace(self._h, tokens, seqs, heads, kv_heads)
+        ws = self._workspace(nbytes)
+        rc = L.prompt_packed(self._h, _PROMPT.pack(
+            q[0], k[0], v[0], o[0], self._lse(lse, heads, tokens) or 0, tokens, q[1], q[2], k[1], k[2], v[1], v[2], o[1], o[2],
+            heads, kv_heads, d, at, seqs, max(tokens, 1) if max_len is None else max_len, scale,
+            ws.data_ptr() if nbytes else 0, nbytes))
+        if rc:
+            self._check(rc)
 
     def _cache(self, cache):
-        _need(cache.device == self.device, "the cache must be on the handle's device")
-        _need(cache.dtype == ("torch.bfloat16" if self.options.dtype == 0 else "torch.float32"),
-              f"the cache holds {cache.dtype}, the handle's options say another type")
-        return ctypes.byref(cache.args)
+        if cache.device != self.device:
+            raise ValueError("the cache must be on the handle's device")
+        if cache.dtype is not (_torch.float32 if self.options.dtype else _torch.bfloat16):
+            raise ValueError(f"the cache holds {cache.dtype}, the handle's options say another type")
+        return cache.args
 
     def tree(self, Q, cache, O, slots, offsets, *, mask=None, max_draft=64, layer=0, scale=1.0, lse=None):
         """Exact attention of drafted tokens (or single ones) over a PagedCache: sequence i (slot slots[i]; None: slot i) has
@@ -342,62 +388,85 @@ class HyperAttention:
         the slot's committed rows. mask [tokens] int64: bit j of a row lets it see drafted row j (None: rows 0..i)."""
         c = self._cache(cache)
         q, o = self._rows(Q, "Q", self.options.dtype), self._rows(O, "O", self._out_dtype())
-        tokens, heads, d = Q.shape
-        _need(O.shape == Q.shape and d == cache.args.d, "Q, O [tokens, heads, d] with the cache's d are needed")
-        _need(offsets.numel() >= 1, "offsets: at least one value is needed")
+        tokens, heads, d = shape = Q.shape
+        if O.shape != shape or d != cache.d:
+            raise ValueError("Q, O [tokens, heads, d] with the cache's d are needed")
+        at = _ints(offsets, self.device, "offsets")
         seqs = offsets.numel() - 1
-        ws = self._workspace(lib().hyper_attn_tree_workspace(self._h, d))
-        a = TreeArgs(q[0], o[0], self._lse(lse, heads, tokens), tokens, q[1], q[2], o[1], o[2], heads, layer,
-                     None if slots is None else _ints(slots, self.device, "slots", seqs),
-                     _ints(offsets, self.device, "offsets"),
-                     None if mask is None else _ints(mask, self.device, "mask", tokens, 64), seqs, max_draft, scale,
-                     ws.data_ptr(), ws.numel())
-        self._check(lib().hyper_attn_tree(self._h, c, ctypes.byref(a)))
+        L = _lib
+        nbytes = L.hyper_attn_tree_workspace(self._h, d)
+        ws = self._workspace(nbytes)
+        rc = L.tree_packed(self._h, c, _TREE.pack(
+            q[0], o[0], self._lse(lse, heads, tokens) or 0, tokens, q[1], q[2], o[1], o[2], heads, layer,
+            0 if slots is None else _ints(slots, self.device, "slots", seqs), at,
+            0 if mask is None else _ints(mask, self.device, "mask", tokens, True), seqs, max_draft, scale,
+            ws.data_ptr() if nbytes else 0, nbytes))
+        if rc:
+            self._check(rc)
 
     def cache_free(self, cache, slots):
         """Release the pages of the given slots (int32 device tensor) and empty them."""
-        self._check(lib().hyper_attn_cache_free(self._h, self._cache(cache), _ints(slots, self.device, "slots"),
-                                                slots.numel()))
+        rc = _lib.hyper_attn_cache_free(self._h, self._cache(cache), _ints(slots, self.device, "slots"), slots.numel())
+        if rc:
+            self._check(rc)
 
     def cache_fork(self, cache, src, dst):
         """Make the empty slots dst copies of the slots src; they share the pages of the committed rows."""
-        self._check(lib().hyper_attn_cache_fork(self._h, self._cache(cache), _ints(src, self.device, "src"),
-                                                _ints(dst, self.device, "dst", src.numel()), src.numel()))
+        n = src.numel()
+        rc = _lib.hyper_attn_cache_fork(self._h, self._cache(cache), _ints(src, self.device, "src"),
+                                        _ints(dst, self.device, "dst", n), n)
+        if rc:
+            self._check(rc)
 
     def cache_reserve(self, cache, slots, add, granted=None):
         """Room for add[i] more rows in slots[i]: new pages, and a copy of a shared last page. granted (int32, optional)
         gets add[i], or 0 where the free pages did not suffice."""
         n = slots.numel()
-        ws = self._workspace(lib().hyper_attn_cache_workspace(n, cache.args.pages))
-        self._check(lib().hyper_attn_cache_reserve(
-            self._h, self._cache(cache), _ints(slots, self.device, "slots"), _ints(add, self.device, "add", n), n,
-            None if granted is None else _ints(granted, self.device, "granted", n), ws.data_ptr(), ws.numel()))
+        L = _lib
+        c = self._cache(cache)
+        nbytes = L.hyper_attn_cache_workspace(n, cache.pages)
+        ws = self._workspace(nbytes)
+        rc = L.hyper_attn_cache_reserve(
+            self._h, c, _ints(slots, self.device, "slots"), _ints(add, self.device, "add", n), n,
+            None if granted is None else _ints(granted, self.device, "granted", n), ws.data_ptr(), nbytes)
+        if rc:
+            self._check(rc)
 
     def cache_append(self, cache, slots, offsets, K, V, *, layer=0):
         """Write K, V [layers, tokens, kv_heads, d] to the cache's layers from `layer` on: rows offsets[i] ..
         offsets[i+1]-1 go behind the committed rows of slots[i] (reserved before)."""
         c = self._cache(cache)
+        strides = []
         for t in (K, V):
-            _need(t.dim() == 4 and (t.shape[3] == 1 or t.stride(3) == 1) and str(t.dtype) == cache.dtype and
-                  t.device.type == "cuda" and t.device.index == self.device,
-                  "K, V: [layers, tokens, kv_heads, d] of the cache's type on the handle's device, contiguous rows")
-        _need(K.shape == V.shape and K.shape[2] == cache.args.kv_heads and K.shape[3] == cache.args.d,
-              "K, V: the cache's kv_heads and d are needed")
+            s = t.stride()
+            if len(s) != 4 or (s[3] != 1 and t.shape[3] != 1) or t.dtype is not cache.dtype or t.get_device() != self.device:
+                raise ValueError("K, V: [layers, tokens, kv_heads, d] of the cache's type on the handle's device, contiguous rows")
+            strides.append(_STRIDES(*s[:3]))
+        shape = K.shape
+        if V.shape != shape or shape[2] != cache.kv_heads or shape[3] != cache.d:
+            raise ValueError("K, V: the cache's kv_heads and d are needed")
         n = slots.numel()
-        strides = [(ctypes.c_int64 * 3)(*t.stride()[:3]) for t in (K, V)]
-        self._check(lib().hyper_attn_cache_append(
-            self._h, c, _ints(slots, self.device, "slots"), _ints(offsets, self.device, "offsets", n + 1), n, K.shape[1],
-            K.data_ptr(), V.data_ptr(), ctypes.byref(strides[0]), ctypes.byref(strides[1]), layer, K.shape[0]))
+        rc = _lib.hyper_attn_cache_append(
+            self._h, c, _ints(slots, self.device, "slots"), _ints(offsets, self.device, "offsets", n + 1), n, shape[1],
+            K.data_ptr(), V.data_ptr(), strides[0], strides[1], layer, shape[0])
+        if rc:
+            self._check(rc)
 
     def cache_commit(self, cache, slots, counts, keep=None):
         """Keep counts[i] of the rows behind the committed ones of slots[i]: the rows keep[i, :counts[i]] (ascending), or
         the first ones; they become committed, the pages behind them are released."""
         n = slots.numel()
+        most = 0
         if keep is not None:
-            _need(keep.dim() == 2 and keep.shape[0] == n, "keep: [n, max_keep] is needed")
-        self._check(lib().hyper_attn_cache_commit(
+            kshape = keep.shape
+            if len(kshape) != 2 or kshape[0] != n:
+                raise ValueError("keep: [n, max_keep] is needed")
+            most = kshape[1]
+        rc = _lib.hyper_attn_cache_commit(
             self._h, self._cache(cache), _ints(slots, self.device, "slots"), _ints(counts, self.device, "counts", n),
-            None if keep is None else _ints(keep, self.device, "keep"), 0 if keep is None else keep.shape[1], n))
+            None if keep is None else _ints(keep, self.device, "keep"), most, n)
+        if rc:
+            self._check(rc)
 
     def debug_copy(self, what: str, level: int, dtype, count: int) -> np.ndarray:
         out = np.zeros(count, dtype)

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ha_internal.h"
 
 namespace ha {
@@ -28,6 +30,19 @@ inline bool launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess;
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory. The attribute is per device and stays: `known` has a bit for each
+// device (of the first 64) on which it was set.
+template <typename K>
+inline bool allow_smem(K kernel, int bytes, std::atomic<uint64_t> *known) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (known->load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    known->fetch_or(bit, std::memory_order_relaxed);
+    return true;
 }
 
 // Sequence i of a prompt call: its first row and length; length 0 and a flag where the offsets are not ascending

@@ -12,6 +12,8 @@
 // the load of a tile votes on non-finite values, and a tile with one and a mask takes the product with a select.
 #include <math.h>
 
+#include <atomic>
+
 #include "ha_common.cuh"
 #include "ha_internal.h"
 #include "ha_serve.cuh"
@@ -440,14 +442,10 @@ __global__ void __launch_bounds__(32 * kJoinRows) tree_join_kernel(const ServeAr
         a.lse[static_cast<int64_t>(head) * a.tokens + j.start + tok] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
 }
 
-template <typename K>
-bool allow_smem(K kernel, int bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-}
-
 template <int D, typename T>
 int prompt_simt(const ServeArgs &a, cudaStream_t st) {
-    if (!allow_smem(prompt_simt_kernel<D, T>, Smem<D>::kBytes)) return -1;
+    static std::atomic<uint64_t> known{0};
+    if (!allow_smem(prompt_simt_kernel<D, T>, Smem<D>::kBytes, &known)) return -1;
     if ((a.tokens * a.group / kBM + a.seqs) * a.kv_heads > 0x7fffffff) return -2;   // blocks of a grid
     const int64_t tiles = a.tokens * a.group / kBM + a.seqs;   // at most: one ragged tile per sequence
     prompt_simt_kernel<D, T><<<static_cast<unsigned>(tiles * a.kv_heads), kThreads, Smem<D>::kBytes, st>>>(a);
@@ -456,7 +454,8 @@ int prompt_simt(const ServeArgs &a, cudaStream_t st) {
 
 template <int D, typename T>
 int tree_simt(const ServeArgs &a, cudaStream_t st) {
-    if (!allow_smem(tree_simt_kernel<D, T>, Smem<D>::kBytes)) return -1;
+    static std::atomic<uint64_t> known{0};
+    if (!allow_smem(tree_simt_kernel<D, T>, Smem<D>::kBytes, &known)) return -1;
     const int blocks = 2 * a.sms;   // two per SM fit (shared memory)
     tree_simt_kernel<D, T><<<blocks, kThreads, Smem<D>::kBytes, st>>>(a);
     if (cudaPeekAtLastError() != cudaSuccess) return -1;

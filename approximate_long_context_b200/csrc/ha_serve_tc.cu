@@ -29,6 +29,9 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <atomic>
+#include <type_traits>
+
 #include "ha_common.cuh"
 #include "ha_internal.h"
 #include "ha_serve.cuh"
@@ -77,8 +80,8 @@ struct Cfg {
     static constexpr int kBars = kStat + (ALT ? 128 * 8 : 0);
     static constexpr int bQFull = 0, bQEmpty = bQFull + 2, bKFull = bQEmpty + 2, bKEmpty = bKFull + NK,
                          bVFull = bKEmpty + NK, bVOk = bVFull + NV, bVEmpty = bVOk + NV, bItemFull = bVEmpty + NV,
-                         bItemEmpty = bItemFull + kItems, bSFull = bItemEmpty + kItems, bPFull = bSFull + 2,
-                         bODone = bPFull + 2, bOFree = bODone + 2, bStat = bOFree + 2, bDrain = bStat + 1,
+                         bItemEmpty = bItemFull + kItems, bSFull = bItemEmpty + kItems, bPHalf = bSFull + 2,
+                         bPFull = bPHalf + 2, bODone = bPFull + 2, bOFree = bODone + 2, bStat = bOFree + 2, bDrain = bStat + 1,
                          kNumBars = bDrain + 1;
     static constexpr int kTmemSlot = kBars + kNumBars * 8;
     static constexpr int kAbort = kTmemSlot + 4;
@@ -273,6 +276,49 @@ __device__ __forceinline__ uint32_t seen_tree(uint64_t bits, int len, int first)
     return static_cast<uint32_t>(bits << -s) | ((1u << -s) - 1u);
 }
 
+// ---------------------------------------------------------------------------------------------- exponentials
+
+// 2^x of two values with fused multiply-adds, for x <= 127: the special-function units give 16 results per SM and cycle,
+// which would bound a 128 x 128 tile at 1024 cycles, as long as its two products of d = 128 take. x = n + f with n the nearest
+// integer (found by adding 1.5 * 2^23, whose unit in the last place is 1) and |f| <= 1/2; 2^f by the polynomial of degree 5
+// with the least largest relative error on [-1/2, 1/2] (Remez exchange; 2.2e-7 with the fp32 roundings, as close as the
+// special-function unit); 2^n by its exponent bits. x is held above -126, where the result no longer counts; NaN stays NaN.
+constexpr int kPolyEvery = 4;   // one pair of every so many
+
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t x, uint64_t y) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_both(float x) { return f2_pack(x, x); }
+
+__device__ __forceinline__ uint64_t exp2_poly(uint64_t x) {
+    float2 v = f2_unpack(x);
+    x = f2_pack(max_nan(v.x, -126.f), max_nan(v.y, -126.f));
+    const uint64_t t = f2_add(x, f2_both(12582912.f));
+    const uint64_t f = f2_sub(x, f2_sub(t, f2_both(12582912.f)));
+    uint64_t p = f2_fma(f2_both(0.0013276472454890609f), f, f2_both(0.009675540961325169f));
+    p = f2_fma(p, f, f2_both(0.05550713092088699f));
+    p = f2_fma(p, f, f2_both(0.24022120237350464f));
+    p = f2_fma(p, f, f2_both(0.6931469440460205f));
+    p = f2_fma(p, f, f2_both(1.0000001192092896f));
+    v = f2_unpack(t);
+    const float a = __uint_as_float((__float_as_uint(v.x) << 23) + 0x3f800000u);
+    const float b = __uint_as_float((__float_as_uint(v.y) << 23) + 0x3f800000u);
+    return f2_mul(p, f2_pack(a, b));
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------------------------------------------- the kernel
 
 template <int D, int MODE>
@@ -295,9 +341,10 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
             mbar_init(bar(C::bQFull + i), 1);
             mbar_init(bar(C::bQEmpty + i), 1);
             mbar_init(bar(C::bSFull + i), 1);
-            mbar_init(bar(C::bPFull + i), 128);
+            mbar_init(bar(C::bPHalf + i), 4);    // one arrival per warp
+            mbar_init(bar(C::bPFull + i), 4);
             mbar_init(bar(C::bODone + i), 1);
-            mbar_init(bar(C::bOFree + i), 128);
+            mbar_init(bar(C::bOFree + i), 4);
         }
         for (int i = 0; i < C::NK; ++i) {
             mbar_init(bar(C::bKFull + i), 1);
@@ -305,14 +352,14 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
         }
         for (int i = 0; i < C::NV; ++i) {
             mbar_init(bar(C::bVFull + i), 1);
-            mbar_init(bar(C::bVOk + i), 64);
+            mbar_init(bar(C::bVOk + i), 2);
             mbar_init(bar(C::bVEmpty + i), 1);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(bar(C::bItemFull + i), 1);
             mbar_init(bar(C::bItemEmpty + i), 11);   // MMA issuer, two looking warps, eight softmax warps
         }
-        mbar_init(bar(C::bStat), 128);
+        mbar_init(bar(C::bStat), 4);
         mbar_init(bar(C::bDrain), 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -335,6 +382,11 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
     // a wait of a whole warp: all of its lanes go on or none
     auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag)); };
     // the item ring, read by all roles but the loader
+    // one arrival for a warp whose lanes have all got here (and fenced what they wrote)
+    auto warp_arrive = [&](uint32_t b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b);
+    };
     auto item_bar = [&](uint32_t i) -> uint32_t { return bar(C::bItemFull + i % kItems); };
 
     if (warp == 0) {
@@ -490,116 +542,137 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false, false);
-            constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
-            const uint64_t dq0 = smem_desc(sbase + C::kQ, 16, 1024);
-            const uint64_t dk0 = smem_desc(sbase + C::kK, 16, 1024);
-            const uint64_t dv0 = smem_desc(sbase + C::kV, 16384, 1024);
-            bool ok = true;
-            struct Unit {
-                uint32_t item;       // number of the item
-                uint32_t base;       // number of the item's first key tile among the block's loads
-                int n0, n1, j, t;
-                bool end;
-            };
-            uint32_t cq[2] = {0, 0};   // items of tile t whose Q has been waited for (ALT: entry 0)
-            uint32_t cp[2] = {0, 0};   // P tiles consumed
-            uint32_t co[2] = {0, 0};   // items of tile t begun (P V)
-            auto tile_of = [&](const Unit &u) -> uint32_t { return u.base + (ALT ? 2 * u.j + u.t : u.j); };
-            auto first_of = [&](Unit &u) {      // first unit of item u.item (published)
-                const Item &it = items[u.item % kItems];
-                u.n0 = it.n0;
-                u.n1 = it.n1;
-                u.end = it.last != 0;
-                u.j = 0;
-                u.t = 0;                         // tile 0 always has keys
-            };
-            // the unit behind u; false if its item is not there yet and block is not set
-            auto advance = [&](const Unit &u, Unit &v, bool block) -> bool {
-                v = u;
-                const int most = max(u.n0, u.n1);
-                do {
-                    if (v.t == 0) v.t = 1;
-                    else { v.t = 0; ++v.j; }
-                } while (v.j < most && v.j >= (v.t == 0 ? v.n0 : v.n1));
-                if (v.j < most) return true;
-                v.item = u.item + 1;
-                v.base = u.base + (ALT ? u.n0 + u.n1 : most);
-                const uint32_t b = bar(C::bItemFull + v.item % kItems), par = (v.item / kItems) & 1;
-                if (block) {
-                    if (!mbar_wait(b, par, abort_flag)) { ok = false; return false; }
-                } else if (!mbar_try_wait(b, par)) {
-                    return false;
-                }
-                first_of(v);
-                return true;
-            };
-            auto issue_s = [&](const Unit &u, bool block) -> bool {
-                const uint32_t tile = tile_of(u);
-                const int s = tile % C::NK, qi = ALT ? 0 : u.t;
-                const bool new_q = u.j == 0 && (!ALT || u.t == 0);
-                const uint32_t kb = bar(C::bKFull + s), kpar = (tile / C::NK) & 1;
-                const uint32_t qb = bar(C::bQFull + qi), qpar = cq[qi] & 1;
-                if (block) {
-                    if (!mbar_wait(kb, kpar, abort_flag) || (new_q && !mbar_wait(qb, qpar, abort_flag))) { ok = false; return false; }
-                } else if (!mbar_try_wait(kb, kpar) || (new_q && !mbar_try_wait(qb, qpar))) {
-                    return false;
-                }
-                if (new_q) ++cq[qi];
-                tc_fence_after();
-                const uint64_t dq = dq0 + static_cast<uint64_t>((qi * C::kTile) >> 4);
-                const uint64_t dk = dk0 + static_cast<uint64_t>((s * C::kTile) >> 4);
+        // The whole warp runs the control flow and one elected lane issues: loop state stays in uniform registers, which
+        // the descriptors of the MMAs have to be in (with a single-lane branch around all of it, 1400 of 2500 cycles per unit
+        // went to moving and waiting between the MMAs).
+        const bool leader = elect_one();
+        constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false, false);
+        constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
+        const uint64_t dq0 = smem_desc(sbase + C::kQ, 16, 1024);
+        const uint64_t dk0 = smem_desc(sbase + C::kK, 16, 1024);
+        const uint64_t dv0 = smem_desc(sbase + C::kV, 16384, 1024);
+        bool ok = true;
+        uint32_t base = 0;                   // number of the item's first key tile among the block's loads
+        uint32_t cq[2] = {0, 0};             // Q tiles waited for (ALT: entry 0)
+        uint32_t cp[2] = {0, 0};             // P tiles consumed
+        uint32_t co[2] = {0, 0};             // items begun
+        int n0 = 0, n1 = 0, last = 0;
+        auto read_item = [&](uint32_t i, int *m0, int *m1, int *end) {
+            const volatile Item &it = items[i % kItems];
+            *m0 = __shfl_sync(0xffffffffu, it.n0, 0);
+            *m1 = __shfl_sync(0xffffffffu, it.n1, 0);
+            *end = __shfl_sync(0xffffffffu, it.last, 0);
+        };
+        // S of tile T's key tile j of an item that begins at load `first` and has (m0, m1) key tiles
+        auto issue_s = [&](auto T, uint32_t first, int j, int m0, int m1, bool block) -> bool {
+            constexpr int t = decltype(T)::value, qi = ALT ? 0 : t;
+            const uint32_t tile = first + (ALT ? 2 * j + t : j);
+            const int s = tile % C::NK;
+            const uint32_t kb = bar(C::bKFull + s), kpar = (tile / C::NK) & 1;
+            const bool new_q = j == 0 && (!ALT || t == 0);
+            if (block) {
+                if (!warp_wait(kb, kpar) || (new_q && !warp_wait(bar(C::bQFull + qi), cq[qi] & 1))) { ok = false; return false; }
+            } else if (!__all_sync(0xffffffffu, mbar_try_wait(kb, kpar)) ||
+                       (new_q && !__all_sync(0xffffffffu, mbar_try_wait(bar(C::bQFull + qi), cq[qi] & 1)))) {
+                return false;
+            }
+            if (new_q) ++cq[qi];
+            tc_fence_after();
+            const uint64_t dq = dq0 + static_cast<uint64_t>((qi * C::kTile) >> 4);
+            const uint64_t dk = dk0 + static_cast<uint64_t>((s * C::kTile) >> 4);
+            const bool free_k = ALT || t == 1 || j >= m1;
+            // the item's last score product with this Q
+            const bool free_q = !ALT ? j == (t == 0 ? m0 : m1) - 1 : t == 0 ? m0 == j + 1 && m1 <= j : m0 <= j + 1;
+            if (leader) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-                    mma_ss(tmem + u.t * 128, dq + off, dk + off, idesc_qk, kk > 0 ? 1u : 0u);
+                    mma_ss(tmem + t * 128, dq + off, dk + off, idesc_qk, kk > 0 ? 1u : 0u);
                 }
-                mma_commit(bar(C::bSFull + u.t));
-                const bool last_user = ALT || u.t == 1 || u.j >= u.n1;
-                if (last_user) mma_commit(bar(C::bKEmpty + s));
-                // the item's last score product with this Q
-                const bool last_q = !ALT ? u.j == (u.t == 0 ? u.n0 : u.n1) - 1
-                                         : u.t == 0 ? u.n0 == u.j + 1 && u.n1 <= u.j : u.n0 <= u.j + 1;
-                if (last_q) mma_commit(bar(C::bQEmpty + qi));
-                return true;
-            };
-            auto issue_pv = [&](const Unit &u) -> bool {
-                const uint32_t tile = tile_of(u);
-                const int s = tile % C::NV;
-                if (!mbar_wait(bar(C::bPFull + u.t), cp[u.t] & 1, abort_flag)) return false;
-                ++cp[u.t];
-                if (!mbar_wait(bar(C::bVOk + s), (tile / C::NV) & 1, abort_flag)) return false;
-                if (u.j == 0) {
-                    if (co[u.t] > 0 && !mbar_wait(bar(C::bOFree + u.t), (co[u.t] - 1) & 1, abort_flag)) return false;
-                    ++co[u.t];
-                }
-                tc_fence_after();
-                const uint64_t dv = dv0 + static_cast<uint64_t>((s * C::kTile) >> 4);
+                mma_commit(bar(C::bSFull + t));
+                if (free_k) mma_commit(bar(C::bKEmpty + s));
+                if (free_q) mma_commit(bar(C::bQEmpty + qi));
+            }
+            __syncwarp();
+            return true;
+        };
+        auto issue_pv = [&](auto T, int j) -> bool {
+            constexpr int t = decltype(T)::value;
+            const uint32_t tile = base + (ALT ? 2 * j + t : j);
+            const int s = tile % C::NV;
+            if (!warp_wait(bar(C::bVOk + s), (tile / C::NV) & 1)) return false;
+            if (j == 0) {
+                if (co[t] > 0 && !warp_wait(bar(C::bOFree + t), (co[t] - 1) & 1)) return false;
+                ++co[t];
+            }
+            const uint64_t dv = dv0 + static_cast<uint64_t>((s * C::kTile) >> 4);
+            const uint32_t par = cp[t] & 1;
+            ++cp[t];
+            const bool free_v = ALT || t == 1 || j >= n1;
+            const bool done = j == (t == 0 ? n0 : n1) - 1;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ts(tmem + 256 + u.t * D, tmem + u.t * 128 + kk * 8, dv + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
-                           (u.j > 0 || kk > 0) ? 1u : 0u);
-                if (ALT || u.t == 1 || u.j >= u.n1) mma_commit(bar(C::bVEmpty + s));
-                if (u.j == (u.t == 0 ? u.n0 : u.n1) - 1) mma_commit(bar(C::bODone + u.t));
-                return true;
-            };
-            Unit cur{}, nxt{};
-            ok = mbar_wait(item_bar(0), 0, abort_flag);
-            if (ok) {
-                first_of(cur);
-                if (!cur.end) ok = issue_s(cur, true);
+            for (int half = 0; half < 2; ++half) {   // P arrives in two halves of 64 keys
+                if (!warp_wait(bar((half ? C::bPFull : C::bPHalf) + t), par)) return false;
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+                        mma_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8, dv + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+                    if (half) {
+                        if (free_v) mma_commit(bar(C::bVEmpty + s));
+                        if (done) mma_commit(bar(C::bODone + t));
+                    }
+                }
+                __syncwarp();
             }
-            while (ok && !cur.end) {
-                bool known = advance(cur, nxt, false), issued = false;
-                if (known && !nxt.end && nxt.t != cur.t) issued = issue_s(nxt, false);
-                if (!issue_pv(cur)) { ok = false; break; }
-                if (!known && !advance(cur, nxt, true)) break;
-                if (nxt.item != cur.item) mbar_arrive(bar(C::bItemEmpty + cur.item % kItems));
-                if (!nxt.end && !issued && !issue_s(nxt, true)) break;
-                cur = nxt;
+            return true;
+        };
+        const std::integral_constant<int, 0> t0;
+        const std::integral_constant<int, 1> t1;
+        uint32_t idx = 0;
+        bool s0 = false, s1 = false;   // first score products of the item already issued
+        ok = warp_wait(item_bar(0), 0);
+        if (ok) read_item(0, &n0, &n1, &last);
+        while (ok && !last) {
+            if (!s0 && !issue_s(t0, base, 0, n0, n1, true)) break;
+            if (n1 > 0 && !s1 && !issue_s(t1, base, 0, n0, n1, true)) break;
+            s0 = s1 = false;
+            const int most = max(n0, n1);
+            const uint32_t next = base + (ALT ? n0 + n1 : most);
+            int m0 = 0, m1 = 0, end = 1;
+            bool known = false;
+            for (int j = 0; j < most; ++j) {
+                const bool fin = j == most - 1;
+                if (fin) {
+                    known = __all_sync(0xffffffffu, mbar_try_wait(item_bar(idx + 1), ((idx + 1) / kItems) & 1));
+                    if (known) read_item(idx + 1, &m0, &m1, &end);
+                }
+                if (j < n0) {
+                    if (!issue_pv(t0, j)) { ok = false; break; }
+                    if (j + 1 < n0 && !issue_s(t0, base, j + 1, n0, n1, true)) break;
+                }
+                if (fin && known && !end) s0 = issue_s(t0, next, 0, m0, m1, false);
+                if (j < n1) {
+                    if (!issue_pv(t1, j)) { ok = false; break; }
+                    if (j + 1 < n1 && !issue_s(t1, base, j + 1, n0, n1, true)) break;
+                }
+                if (s0 && m1 > 0) s1 = issue_s(t1, next, 0, m0, m1, false);
             }
-            if (!ok) atomicOr(a.status, kStatusTimeout);
+            if (!ok) break;
+            if (leader) mbar_arrive(bar(C::bItemEmpty + idx % kItems));
+            ++idx;
+            if (!known) {
+                if (!warp_wait(item_bar(idx), (idx / kItems) & 1)) { ok = false; break; }
+                read_item(idx, &m0, &m1, &end);
+            }
+            base = next;
+            n0 = m0;
+            n1 = m1;
+            last = end;
+        }
+        if (!ok && leader) atomicOr(a.status, kStatusTimeout);
+        if (leader) {
             mma_commit(bar(C::bDrain));   // every MMA issued so far completes before TMEM is released
             volatile int no_abort = 0;
             mbar_wait(bar(C::bDrain), 0, &no_abort, 200000000ull);
@@ -641,7 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                     if (odd) it->odd = 1;
                     fence_proxy_async_smem();
                 }
-                mbar_arrive(bar(C::bVOk + s));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::bVOk + s));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bItemEmpty + i % kItems));
@@ -677,10 +751,12 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                 if (active) {
                     const int kt = k0 + (ALT ? 2 * j + t : j);
                     uint32_t s[4][32];
+                    float top[4];
+                    const bool hide = kt >= masked;
 #pragma unroll
                     for (int h = 0; h < 4; ++h) tmem_ld32(tS + h * 32, s[h]);
                     tmem_ld_wait();
-                    if (kt >= masked) {
+                    if (hide) {
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             const int first = kt * 128 + h * 32;
@@ -690,7 +766,6 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                                 if (!(seen >> e & 1u)) s[h][e] = 0xff800000u;
                         }
                     }
-                    float top[4];
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         top[h] = fmaxf(__uint_as_float(s[h][0]), __uint_as_float(s[h][1]));
@@ -698,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                         for (int e = 2; e < 32; e += 2)
                             top[h] = fmax3(top[h], __uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]));
                     }
-                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+                    const float mx = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * c;
                     const bool grow = mx > m + kGrow;
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to = grow ? mx : m;
@@ -720,25 +795,44 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                     const float ref = m == -INFINITY ? 0.f : m;
                     const uint64_t off = f2_pack(-ref, -ref);
                     uint64_t sum = f2_pack(0.f, 0.f), sum2 = sum;
+                    auto exponentials = [&](auto poly) {
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t pk[16];
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t pk[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[h][2 * e]), __uint_as_float(s[h][2 * e + 1])), c2, off));
-                            const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
-                            if (e & 1) sum = f2_add(sum, f2_pack(p0, p1));
-                            else sum2 = f2_add(sum2, f2_pack(p0, p1));
-                            pk[e] = pack_bf16x2(p0, p1);
+                            for (int e = 0; e < 16; ++e) {
+                                const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[h][2 * e]), __uint_as_float(s[h][2 * e + 1])), c2, off);
+                                uint64_t pr;
+                                if (decltype(poly)::value && e % kPolyEvery == kPolyEvery - 1) {
+                                    pr = exp2_poly(y);
+                                } else {
+                                    const float2 z = f2_unpack(y);
+                                    pr = f2_pack(ex2_approx(z.x), ex2_approx(z.y));
+                                }
+                                if (e & 1) sum = f2_add(sum, pr);
+                                else sum2 = f2_add(sum2, pr);
+                                const float2 z = f2_unpack(pr);
+                                pk[e] = pack_bf16x2(z.x, z.y);
+                            }
+                            tmem_st16(tS + h * 16, pk);
+                            if (h == 1) {
+                                tmem_st_wait();
+                                tc_fence_before();
+                                warp_arrive(bar(C::bPHalf + t));
+                            }
                         }
-                        tmem_st16(tS + h * 16, pk);
-                    }
+                    };
+                    // masked scores (-inf) must give exact zeros, which the polynomial does not
+                    if (hide || __any_sync(0xffffffffu, mx == -INFINITY)) exponentials(std::false_type());
+                    else exponentials(std::true_type());
                     const float2 both = f2_unpack(f2_add(sum, sum2));
                     l += both.x + both.y;
                     tmem_st_wait();
+                } else {
+                    warp_arrive(bar(C::bPHalf + t));
                 }
                 tc_fence_before();
-                mbar_arrive(bar(C::bPFull + t));
+                warp_arrive(bar(C::bPFull + t));
             }
             if (!ok) break;
             // ---- epilogue
@@ -749,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                     if (!warp_wait(bar(C::bODone + 1), no & 1)) { ok = false; break; }
                     ++no;
                     stat[r] = make_float2(m, l);
-                    mbar_arrive(bar(C::bStat));
+                    warp_arrive(bar(C::bStat));
                 }
             } else if (n > 0) {
                 if (!warp_wait(bar(C::bODone + t), no & 1)) { ok = false; break; }
@@ -859,8 +953,8 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(bar(C::bOFree + t));
-                if (join) mbar_arrive(bar(C::bOFree + 1));
+                warp_arrive(bar(C::bOFree + t));
+                if (join) warp_arrive(bar(C::bOFree + 1));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bItemEmpty + i % kItems));
@@ -920,8 +1014,8 @@ bool make_rows_map(CUtensorMap *map, const void *base, int d, int heads, int64_t
 template <int D, int MODE>
 bool launch(const TcArgs &x, const Maps &maps, int blocks, bool dependent, cudaStream_t st) {
     using C = Cfg<D, MODE>;
-    if (cudaFuncSetAttribute(serve_tc_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes) != cudaSuccess)
-        return false;
+    static std::atomic<uint64_t> known{0};
+    if (!allow_smem(serve_tc_kernel<D, MODE>, C::kBytes, &known)) return false;
     if (dependent) return launch_dependent(serve_tc_kernel<D, MODE>, dim3(blocks), dim3(kThreads), C::kBytes, st, x, maps);
     serve_tc_kernel<D, MODE><<<blocks, kThreads, C::kBytes, st>>>(x, maps);
     return cudaPeekAtLastError() == cudaSuccess;
@@ -930,10 +1024,16 @@ bool launch(const TcArgs &x, const Maps &maps, int blocks, bool dependent, cudaS
 // Items of a prompt call: every sequence has at most one pair of tiles that is not full.
 int64_t prompt_items(int64_t tokens, int64_t seqs, int tpt) { return tokens / (2 * tpt) + seqs; }
 
+// Whether the items are listed by a kernel of their own: not for one sequence, whose items are known, nor for fewer
+// items than blocks, which need no order (the extra launch takes about 3 us).
+bool prompt_plan(int64_t tokens, int64_t seqs, int kv_heads, int group, int sms) {
+    return seqs > 1 && prompt_items(tokens, seqs, 128 / group) * kv_heads > sms;
+}
+
 }  // namespace
 
-size_t serve_prompt_workspace(int64_t tokens, int64_t seqs, int group) {
-    if (group > 128) return 0;
+size_t serve_prompt_workspace(int64_t tokens, int64_t seqs, int kv_heads, int group, int sms) {
+    if (group > 128 || !prompt_plan(tokens, seqs, kv_heads, group, sms)) return 0;
     return sizeof(PromptPlan) + static_cast<size_t>(prompt_items(tokens, seqs, 128 / group)) * sizeof(int2);
 }
 
@@ -945,7 +1045,7 @@ int launch_prompt_tc(const ServeArgs &a, cudaStream_t st) {
     x.box_rows = box_tokens * a.group;
     const int64_t items = prompt_items(a.tokens, a.seqs, x.tpt);
     if (items > 0x7fffffff) return -2;
-    x.plan = a.seqs > 1 && items * a.kv_heads > a.sms;
+    x.plan = prompt_plan(a.tokens, a.seqs, a.kv_heads, a.group, a.sms);
     Maps maps;
     if (!make_rows_map(&maps.q, a.q, a.d, a.heads, a.tokens, a.q_head, a.q_tok, a.group, box_tokens) ||
         !make_rows_map(&maps.k, a.k, a.d, a.kv_heads, a.tokens, a.k_head, a.k_tok, 1, 128) ||

@@ -37,6 +37,14 @@ def test_structs_mirror_the_header(tmp_path, c, py):
         assert int(out[f]) == getattr(py, f).offset, f
 
 
+@pytest.mark.parametrize("packed,py", [(binding._PROMPT, binding.PromptArgs), (binding._TREE, binding.TreeArgs)])
+def test_packed_arguments_are_the_struct(packed, py):
+    values = list(range(3, 3 + len(py._fields_)))
+    raw = packed.pack(*values)
+    a = py.from_buffer_copy(raw + bytes(ctypes.sizeof(py) - len(raw)))
+    assert [getattr(a, f) for f, _ in py._fields_] == values
+
+
 def test_null_handles_and_workspaces(lib):
     inv = binding.HA_ERR_INVALID_ARG
     assert lib.hyper_attn_prompt(None, binding.PromptArgs()) == inv
@@ -47,7 +55,7 @@ def test_null_handles_and_workspaces(lib):
     assert lib.hyper_attn_cache_append(None, binding.CacheArgs(), None, None, 0, 0, None, None, None, None, 0, 1) == inv
     assert lib.hyper_attn_cache_commit(None, binding.CacheArgs(), None, None, None, 0, 0) == inv
     assert lib.hyper_attn_tree_workspace(None, 64) == 0
-    assert lib.hyper_attn_prompt_workspace(-1, 1, 1, 1) == 0 and lib.hyper_attn_prompt_workspace(1, 1, 3, 2) == 0
+    assert lib.hyper_attn_prompt_workspace(None, 1, 1, 1, 1) == 0
     assert lib.hyper_attn_cache_workspace(-1, 5) == 0
     assert lib.hyper_attn_cache_workspace(7, 5) >= 7 * 8
 
