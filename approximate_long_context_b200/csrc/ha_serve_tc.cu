@@ -23,9 +23,10 @@
 // value tile over that some row does not see in full, replace what is not finite by 0 before the product and note it
 // for the item; the epilogue of a noted item adds those values to the rows that do see them.
 //
-// Block (384 threads, one per SM, persistent): warp 0 fetches the items and loads (TMA), warp 1 issues the MMAs, warps 2
-// and 3 look values over, warps 4-7 and 8-11 are the softmax of tile 0 and 1. Every wait is bounded; on expiry the status
-// word is set, all roles stop, the loader waits for its copies and TMEM is freed.
+// Block (512 threads, one per SM, persistent): warp 0 fetches the items and loads (TMA), warp 1 issues the MMAs, warps 2
+// and 3 look values over, warps 4-7 and 8-11 are the softmax of tile 0 and 1, warps 12-15 the epilogue of both (a tile's
+// epilogue takes as long as one or two of its units; the softmax goes on with the next item meanwhile). Every wait is
+// bounded; on expiry the status word is set, all roles stop, the loader waits for its copies and TMEM is freed.
 #include <cuda.h>
 #include <math.h>
 
@@ -42,7 +43,11 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
+// Registers per thread of the four warpgroups after the start (512 threads start with 128 each): loads, MMAs and checks;
+// softmax (two); epilogue.
+constexpr int kRegsAux = 80, kRegsSoftmax = 168, kRegsOut = 96;
+static_assert(kRegsAux + 2 * kRegsSoftmax + kRegsOut <= 512, "the shares add up to what the block starts with");
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.0f;
@@ -59,7 +64,7 @@ struct Item {
     int odd;                        // a value that is not finite was replaced
     int64_t kv;                     // tree: row of the page table; prompt: first key row
     int k1;
-    int pad;
+    int duo;                        // two key heads kh, kh + 1 of one query tile each, with key tiles of their own
 };
 static_assert(sizeof(Item) == 64, "one item per 64 bytes");
 
@@ -70,22 +75,24 @@ struct Cfg {
     static constexpr bool ALT = MODE == TREE_ALT;
     static constexpr int kTile = 128 * D * 2;      // 128 rows of bf16
     static constexpr int NQ = ALT ? 1 : 2;
-    static constexpr int NK = D == 64 ? 6 : 3;
-    static constexpr int NV = D == 64 ? (ALT ? 6 : 5) : (ALT ? 3 : 2);
+    static constexpr int NK = D == 64 ? (ALT ? 6 : 5) : (ALT ? 3 : 2);
+    static constexpr int NV = D == 64 ? (ALT ? 6 : 4) : (ALT ? 3 : 2);
     static constexpr int kQ = 0;
     static constexpr int kK = NQ * kTile;
     static constexpr int kV = kK + NK * kTile;
-    static constexpr int kItemsAt = kV + NV * kTile;
-    static constexpr int kStat = kItemsAt + kItems * 64;           // ALT: maximum and sum of tile 1's rows
-    static constexpr int kBars = kStat + (ALT ? 128 * 8 : 0);
+    static constexpr int kOut = kV + NV * kTile;                   // PAIR: 32 rows of 128 bytes per epilogue warp
+    static constexpr int kItemsAt = kOut + 4 * (ALT ? 0 : 4096);
+    static constexpr int kStat = kItemsAt + kItems * 64;           // maximum and sum of the tiles' rows
+    static constexpr int kBars = kStat + 2 * 128 * 8;
     static constexpr int bQFull = 0, bQEmpty = bQFull + 2, bKFull = bQEmpty + 2, bKEmpty = bKFull + NK,
                          bVFull = bKEmpty + NK, bVOk = bVFull + NV, bVEmpty = bVOk + NV, bItemFull = bVEmpty + NV,
-                         bItemEmpty = bItemFull + kItems, bSFull = bItemEmpty + kItems, bPHalf = bSFull + 2,
-                         bPFull = bPHalf + 2, bODone = bPFull + 2, bOFree = bODone + 2, bStat = bOFree + 2, bDrain = bStat + 1,
+                         bItemEmpty = bItemFull + kItems, bSFull = bItemEmpty + kItems, bPFull = bSFull + 2,
+                         bODone = bPFull + 2, bOFree = bODone + 2, bStat = bOFree + 2, bStatFree = bStat + 2,
+                         bDrain = bStatFree + 2,
                          kNumBars = bDrain + 1;
     static constexpr int kTmemSlot = kBars + kNumBars * 8;
     static constexpr int kAbort = kTmemSlot + 4;
-    static constexpr int kBytes = kAbort + 4 + 1024;               // and room to align the base to 1024
+    static constexpr int kBytes = kAbort + 4;
     static_assert(kBars % 8 == 0, "mbarriers need 8-byte alignment");
     static_assert(kBytes <= 232448, "shared memory budget");
 };
@@ -125,20 +132,23 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 4096;
 
 struct PromptPlan {
-    int count;
-    int pad[3];
+    int count;     // entries
+    int single;    // of them, at the end: sequences of one query tile, whose items take two key heads at a time
+    int pad[2];
 };
 
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const ServeArgs a, int pair_tokens, int capacity) {
     __shared__ int cursor[kPlanBuckets];
+    __shared__ int singles;
     __shared__ int sums[32];
     PromptPlan *head = static_cast<PromptPlan *>(a.ws);
     int2 *list = reinterpret_cast<int2 *>(head + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int levels = (a.max_len + pair_tokens - 1) / pair_tokens;
     int shift = 0;
-    while ((levels - 1) >> shift >= kPlanBuckets) ++shift;
-    const int buckets = ((levels - 1) >> shift) + 1;
+    while (((levels - 1) >> shift) + 2 > kPlanBuckets) ++shift;
+    const int buckets = ((levels - 1) >> shift) + 2;   // the last one: sequences of one query tile
+    auto bucket = [&](int p, int len) { return 2 * len <= pair_tokens ? buckets - 1 : buckets - 2 - (p >> shift); };
     for (int b = tid; b < buckets; b += kPlanThreads) cursor[b] = 0;
     __syncthreads();
     bool ok = true;
@@ -146,10 +156,11 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const ServeAr
         int start, len;
         ok &= prompt_seq(a, s, &start, &len);
         const int pairs = (len + pair_tokens - 1) / pair_tokens;
-        for (int p = lane; p < pairs; p += 32) atomicAdd(&cursor[buckets - 1 - (p >> shift)], 1);
+        for (int p = lane; p < pairs; p += 32) atomicAdd(&cursor[bucket(p, len)], 1);
     }
     if (!ok && lane == 0) atomicOr(a.status, kStatusData);
     __syncthreads();
+    if (tid == 0) singles = cursor[buckets - 1];
     // exclusive sums over the buckets, highest position first: four buckets per thread
     int mine[kPlanBuckets / kPlanThreads], sum = 0;
 #pragma unroll
@@ -182,22 +193,26 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const ServeAr
         const int b = tid * (kPlanBuckets / kPlanThreads) + i;
         if (b < buckets) cursor[b] = before + mine[i];
     }
-    if (tid == 0) head->count = min(sums[31], capacity);   // overlapping sequences (reported) could ask for more
+    if (tid == 0) {
+        head->count = min(sums[31], capacity);   // overlapping sequences (reported) could ask for more
+        head->single = max(0, singles - (sums[31] - head->count));
+    }
     __syncthreads();
     for (int s = warp; s < a.seqs; s += 32) {
         int start, len;
         prompt_seq(a, s, &start, &len);
         const int pairs = (len + pair_tokens - 1) / pair_tokens;
         for (int p = lane; p < pairs; p += 32) {
-            const int at = atomicAdd(&cursor[buckets - 1 - (p >> shift)], 1);
+            const int at = atomicAdd(&cursor[bucket(p, len)], 1);
             if (at < capacity) list[at] = make_int2(s, p);
         }
     }
 }
 
-// The block's own copy of the walk over a prompt call's items: (sequence, pair) of item i.
+// The walk of one block over a prompt call's items, run by one whole warp.
 struct PromptWalk {
-    int64_t count;    // items times key heads
+    int64_t count;    // items
+    int64_t normal;   // of them, in front: one key head each
     int64_t round;
     // One sequence, or few enough items for one round of blocks: no list.
     __device__ __forceinline__ void begin(const TcArgs &x) {
@@ -205,7 +220,9 @@ struct PromptWalk {
         const int lane = threadIdx.x & 31;
         round = 0;
         if (x.plan) {
-            count = static_cast<int64_t>(static_cast<const PromptPlan *>(a.ws)->count) * a.kv_heads;
+            const PromptPlan *p = static_cast<const PromptPlan *>(a.ws);
+            normal = static_cast<int64_t>(p->count - p->single) * a.kv_heads;
+            count = normal + static_cast<int64_t>(p->single) * ((a.kv_heads + 1) >> 1);
             return;
         }
         int64_t pairs = 0;
@@ -218,23 +235,27 @@ struct PromptWalk {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
         if (!ok && blockIdx.x == 0) atomicOr(a.status, kStatusData);
-        count = pairs * a.kv_heads;
+        normal = count = pairs * a.kv_heads;
     }
-    __device__ __forceinline__ bool next(const TcArgs &x, int *seq, int *pair, int *kh) {
+    __device__ __forceinline__ bool next(const TcArgs &x, int *seq, int *pair, int *kh, bool *single) {
         const ServeArgs &a = x.a;
         const int lane = threadIdx.x & 31;
         const int64_t turn = (round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
         const int64_t i = round * gridDim.x + turn;
         ++round;
         if (i >= count) return false;   // the last round is not full
-        *kh = static_cast<int>(i % a.kv_heads);
-        const int64_t at = i / a.kv_heads;
         if (x.plan) {
+            const int half = (a.kv_heads + 1) >> 1;
+            *single = i >= normal;
+            const int64_t at = *single ? normal / a.kv_heads + (i - normal) / half : i / a.kv_heads;
+            *kh = *single ? 2 * static_cast<int>((i - normal) % half) : static_cast<int>(i % a.kv_heads);
             const int2 e = reinterpret_cast<const int2 *>(static_cast<const PromptPlan *>(a.ws) + 1)[at];
             *seq = e.x;
             *pair = e.y;
             return true;
         }
+        *kh = static_cast<int>(i % a.kv_heads);
+        const int64_t at = i / a.kv_heads;
         int64_t run = 0;
         for (int b = 0; b < a.seqs; b += 32) {
             int start = 0, len = 0;
@@ -276,43 +297,6 @@ __device__ __forceinline__ uint32_t seen_tree(uint64_t bits, int len, int first)
     return static_cast<uint32_t>(bits << -s) | ((1u << -s) - 1u);
 }
 
-// ---------------------------------------------------------------------------------------------- exponentials
-
-// 2^x of two values with fused multiply-adds, for x <= 127: the special-function units give 16 results per SM and cycle,
-// which would bound a 128 x 128 tile at 1024 cycles, as long as its two products of d = 128 take. x = n + f with n the nearest
-// integer (found by adding 1.5 * 2^23, whose unit in the last place is 1) and |f| <= 1/2; 2^f by the polynomial of degree 5
-// with the least largest relative error on [-1/2, 1/2] (Remez exchange; 2.2e-7 with the fp32 roundings, as close as the
-// special-function unit); 2^n by its exponent bits. x is held above -126, where the result no longer counts; NaN stays NaN.
-constexpr int kPolyEvery = 4;   // one pair of every so many
-
-__device__ __forceinline__ float max_nan(float x, float y) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(y));
-    return d;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t x, uint64_t y) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
-    return d;
-}
-__device__ __forceinline__ uint64_t f2_both(float x) { return f2_pack(x, x); }
-
-__device__ __forceinline__ uint64_t exp2_poly(uint64_t x) {
-    float2 v = f2_unpack(x);
-    x = f2_pack(max_nan(v.x, -126.f), max_nan(v.y, -126.f));
-    const uint64_t t = f2_add(x, f2_both(12582912.f));
-    const uint64_t f = f2_sub(x, f2_sub(t, f2_both(12582912.f)));
-    uint64_t p = f2_fma(f2_both(0.0013276472454890609f), f, f2_both(0.009675540961325169f));
-    p = f2_fma(p, f, f2_both(0.05550713092088699f));
-    p = f2_fma(p, f, f2_both(0.24022120237350464f));
-    p = f2_fma(p, f, f2_both(0.6931469440460205f));
-    p = f2_fma(p, f, f2_both(1.0000001192092896f));
-    v = f2_unpack(t);
-    const float a = __uint_as_float((__float_as_uint(v.x) << 23) + 0x3f800000u);
-    const float b = __uint_as_float((__float_as_uint(v.y) << 23) + 0x3f800000u);
-    return f2_mul(p, f2_pack(a, b));
-}
-
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -326,11 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
     using C = Cfg<D, MODE>;
     constexpr bool ALT = C::ALT, TREE = MODE != PROMPT;
     const ServeArgs &a = x.a;
-    extern __shared__ unsigned char smem_raw[];
-    const uint32_t raw_addr = smem_addr(smem_raw);
-    const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
-    unsigned char *sm = smem_raw + pad;
-    const uint32_t sbase = raw_addr + pad;
+    extern __shared__ __align__(1024) unsigned char sm[];   // the swizzled tiles need the alignment; there is no room to pad
+    const uint32_t sbase = smem_addr(sm);
+    if (sbase & 1023u) {
+        if (threadIdx.x == 0) atomicOr(a.status, kStatusTimeout);
+        return;
+    }
     auto bar = [&](int i) -> uint32_t { return sbase + C::kBars + 8u * static_cast<uint32_t>(i); };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::kAbort);
     Item *items = reinterpret_cast<Item *>(sm + C::kItemsAt);
@@ -341,8 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
             mbar_init(bar(C::bQFull + i), 1);
             mbar_init(bar(C::bQEmpty + i), 1);
             mbar_init(bar(C::bSFull + i), 1);
-            mbar_init(bar(C::bPHalf + i), 4);    // one arrival per warp
-            mbar_init(bar(C::bPFull + i), 4);
+            mbar_init(bar(C::bPFull + i), 4);    // one arrival per warp
             mbar_init(bar(C::bODone + i), 1);
             mbar_init(bar(C::bOFree + i), 4);
         }
@@ -357,9 +341,12 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(bar(C::bItemFull + i), 1);
-            mbar_init(bar(C::bItemEmpty + i), 11);   // MMA issuer, two looking warps, eight softmax warps
+            mbar_init(bar(C::bItemEmpty + i), 1 + 2 + 8 + 4);   // MMA issuer, looking, softmax and epilogue warps
         }
-        mbar_init(bar(C::bStat), 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(C::bStat + i), 4);
+            mbar_init(bar(C::bStatFree + i), 4);
+        }
         mbar_init(bar(C::bDrain), 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -380,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
     grid_dependency_wait();   // the list of prompt items, if a kernel in front of this one makes it
 
     // a wait of a whole warp: all of its lanes go on or none
-    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag)); };
+    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait_inl(b, parity, abort_flag)); };
     // the item ring, read by all roles but the loader
     // one arrival for a warp whose lanes have all got here (and fenced what they wrote)
     auto warp_arrive = [&](uint32_t b) {
@@ -391,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
 
     if (warp == 0) {
         // ------------------------------------------------------------------ items and loads
+        setmaxnreg_dec<kRegsAux>();
         bool ok = true;
         uint32_t ni = 0, nk = 0, nv = 0, nq[2] = {0, 0};   // items published, loads issued
         PromptWalk pw;
@@ -435,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                 }
             } else {
                 int seq, pair, kh;
-                got = pw.next(x, &seq, &pair, &kh);
+                bool single = false;
+                got = pw.next(x, &seq, &pair, &kh, &single);
                 if (got) {
                     prompt_seq(a, seq, &it.start, &it.tokens);
                     it.tok0 = pair * 2 * x.tpt;
@@ -445,6 +434,10 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                     it.kv = it.start;
                     it.n0 = (min(it.tokens, it.tok0 + x.tpt) + 127) >> 7;
                     it.n1 = it.tok0 + x.tpt < it.tokens ? (min(it.tokens, it.tok0 + 2 * x.tpt) + 127) >> 7 : 0;
+                    if (single) {
+                        it.duo = 1;
+                        it.n1 = kh + 1 < a.kv_heads ? it.n0 : 0;
+                    }
                     it.k1 = max(it.n0, it.n1);
                 }
             }
@@ -458,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
             __syncwarp();
             ++ni;
             if (!got) break;
-            const int n = it.k1 - it.k0;
+            const int n = it.duo ? it.n0 + it.n1 : it.k1 - it.k0;
             const int keys = it.len + it.tokens;
             // page of this lane's part of key tile j (tree), -1 where the load is to bring zeros
             auto page_of = [&](int kt) -> int {
@@ -475,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                 }
                 return id;
             };
-            auto load_tile = [&](const CUtensorMap *map, uint32_t dst, uint32_t b, int kt, int id) {
+            auto load_tile = [&](const CUtensorMap *map, uint32_t dst, uint32_t b, int i, int id) {
+                const int kt = it.k0 + (it.duo ? i >> 1 : i), kh = it.kh + (it.duo ? i & 1 : 0);
                 if (lane == 0) mbar_arrive_expect_tx(b, C::kTile);
                 __syncwarp();
                 if (TREE) {
@@ -484,29 +478,29 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                         const int y = page > 128 ? (kt * 128) & (page - 1) : 0;
 #pragma unroll
                         for (int h = 0; h < D / 64; ++h)
-                            tma_4d(dst + h * 16384 + lane * (page << 7), map, b, h * 64, y, it.kh, z);
+                            tma_4d(dst + h * 16384 + lane * (page << 7), map, b, h * 64, y, kh, z);
                     }
                 } else if (lane == 0) {
 #pragma unroll
-                    for (int h = 0; h < D / 64; ++h) tma_3d(dst + h * 16384, map, b, h * 64, it.kh, static_cast<int>(it.kv) + kt * 128);
+                    for (int h = 0; h < D / 64; ++h) tma_3d(dst + h * 16384, map, b, h * 64, kh, static_cast<int>(it.kv) + kt * 128);
                 }
             };
-            auto load_k = [&](int kt, int id) -> bool {
+            auto load_k = [&](int i, int id) -> bool {
                 const int s = nk % C::NK;
                 if (nk >= C::NK && !warp_wait(bar(C::bKEmpty + s), (nk / C::NK - 1) & 1)) return false;
-                load_tile(&maps.k, sbase + C::kK + s * C::kTile, bar(C::bKFull + s), kt, id);
+                load_tile(&maps.k, sbase + C::kK + s * C::kTile, bar(C::bKFull + s), i, id);
                 ++nk;
                 return true;
             };
-            auto load_v = [&](int kt, int id) -> bool {
+            auto load_v = [&](int i, int id) -> bool {
                 const int s = nv % C::NV;
                 if (nv >= C::NV && !warp_wait(bar(C::bVEmpty + s), (nv / C::NV - 1) & 1)) return false;
-                load_tile(&maps.v, sbase + C::kV + s * C::kTile, bar(C::bVFull + s), kt, id);
+                load_tile(&maps.v, sbase + C::kV + s * C::kTile, bar(C::bVFull + s), i, id);
                 ++nv;
                 return true;
             };
             int id = page_of(it.k0), ahead = n > 1 ? page_of(it.k0 + 1) : -1;
-            ok = load_k(it.k0, id);
+            ok = load_k(0, id);
             for (int t = 0; t < C::NQ && ok; ++t) {
                 if (!ALT && (t == 0 ? it.n0 : it.n1) == 0) continue;
                 if (nq[t] >= 1 && !warp_wait(bar(C::bQEmpty + t), (nq[t] - 1) & 1)) { ok = false; break; }
@@ -514,16 +508,16 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                     mbar_arrive_expect_tx(bar(C::bQFull + t), x.box_rows * D * 2);
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h)
-                        tma_3d(sbase + C::kQ + t * C::kTile + h * 16384, &maps.q, bar(C::bQFull + t), h * 64, it.kh * a.group,
-                               it.start + it.tok0 + t * x.tpt);
+                        tma_3d(sbase + C::kQ + t * C::kTile + h * 16384, &maps.q, bar(C::bQFull + t), h * 64,
+                               (it.kh + (it.duo ? t : 0)) * a.group, it.start + it.tok0 + (it.duo ? 0 : t * x.tpt));
                 }
                 __syncwarp();
                 ++nq[t];
             }
             for (int j = 0; j < n && ok; ++j) {
                 const int far = j + 2 < n ? page_of(it.k0 + j + 2) : -1;
-                if (j + 1 < n) ok = load_k(it.k0 + j + 1, ahead);
-                if (ok) ok = load_v(it.k0 + j, id);
+                if (j + 1 < n) ok = load_k(j + 1, ahead);
+                if (ok) ok = load_v(j, id);
                 id = ahead;
                 ahead = far;
             }
@@ -534,17 +528,19 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
             // the copies in flight land before the block ends
             volatile int no_abort = 0;
             for (uint32_t i = nk > C::NK ? nk - C::NK : 0; i < nk; ++i)
-                mbar_wait(bar(C::bKFull + i % C::NK), (i / C::NK) & 1, &no_abort, 200000000ull);
+                mbar_wait_inl(bar(C::bKFull + i % C::NK), (i / C::NK) & 1, &no_abort, 200000000ull);
             for (uint32_t i = nv > C::NV ? nv - C::NV : 0; i < nv; ++i)
-                mbar_wait(bar(C::bVFull + i % C::NV), (i / C::NV) & 1, &no_abort, 200000000ull);
+                mbar_wait_inl(bar(C::bVFull + i % C::NV), (i / C::NV) & 1, &no_abort, 200000000ull);
             for (int t = 0; t < C::NQ; ++t)
-                if (nq[t]) mbar_wait(bar(C::bQFull + t), (nq[t] - 1) & 1, &no_abort, 200000000ull);
+                if (nq[t]) mbar_wait_inl(bar(C::bQFull + t), (nq[t] - 1) & 1, &no_abort, 200000000ull);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
+        setmaxnreg_dec<kRegsAux>();
         // The whole warp runs the control flow and one elected lane issues: loop state stays in uniform registers, which
-        // the descriptors of the MMAs have to be in (with a single-lane branch around all of it, 1400 of 2500 cycles per unit
-        // went to moving and waiting between the MMAs).
+        // the descriptors of the MMAs have to be in. One copy of each kind of step, looped over: the warp shares its
+        // scheduler's instruction cache with two softmax warps, and a straight-line version spent about 200 cycles per
+        // wait on fetching itself.
         const bool leader = elect_one();
         constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false, false);
         constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
@@ -552,145 +548,134 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
         const uint64_t dk0 = smem_desc(sbase + C::kK, 16, 1024);
         const uint64_t dv0 = smem_desc(sbase + C::kV, 16384, 1024);
         bool ok = true;
-        uint32_t base = 0;                   // number of the item's first key tile among the block's loads
-        uint32_t cq[2] = {0, 0};             // Q tiles waited for (ALT: entry 0)
-        uint32_t cp[2] = {0, 0};             // P tiles consumed
-        uint32_t co[2] = {0, 0};             // items begun
+        uint32_t base = 0, idx = 0;          // number of the item's first key tile among the block's loads; the item
+        uint32_t cq = 0, cp = 0, co = 0;     // parities, bit t: Q tiles waited for (ALT: bit 0), P tiles consumed, items begun
+        uint32_t begun = 0;                  // bit t: tile t has had an item
         int n0 = 0, n1 = 0, last = 0;
-        auto read_item = [&](uint32_t i, int *m0, int *m1, int *end) {
+        bool two = ALT;                      // the tiles take turns at the key tiles (ALT and two heads) or share them
+        auto read_item = [&](uint32_t i, int *m0, int *m1, int *end, bool *turns) {
             const volatile Item &it = items[i % kItems];
             *m0 = __shfl_sync(0xffffffffu, it.n0, 0);
             *m1 = __shfl_sync(0xffffffffu, it.n1, 0);
             *end = __shfl_sync(0xffffffffu, it.last, 0);
+            *turns = ALT || (!TREE && __shfl_sync(0xffffffffu, it.duo, 0) != 0);
         };
-        // S of tile T's key tile j of an item that begins at load `first` and has (m0, m1) key tiles
-        auto issue_s = [&](auto T, uint32_t first, int j, int m0, int m1, bool block) -> bool {
-            constexpr int t = decltype(T)::value, qi = ALT ? 0 : t;
-            const uint32_t tile = first + (ALT ? 2 * j + t : j);
-            const int s = tile % C::NK;
-            const uint32_t kb = bar(C::bKFull + s), kpar = (tile / C::NK) & 1;
-            const bool new_q = j == 0 && (!ALT || t == 0);
-            if (block) {
-                if (!warp_wait(kb, kpar) || (new_q && !warp_wait(bar(C::bQFull + qi), cq[qi] & 1))) { ok = false; return false; }
-            } else if (!__all_sync(0xffffffffu, mbar_try_wait(kb, kpar)) ||
-                       (new_q && !__all_sync(0xffffffffu, mbar_try_wait(bar(C::bQFull + qi), cq[qi] & 1)))) {
-                return false;
-            }
-            if (new_q) ++cq[qi];
-            tc_fence_after();
-            const uint64_t dq = dq0 + static_cast<uint64_t>((qi * C::kTile) >> 4);
-            const uint64_t dk = dk0 + static_cast<uint64_t>((s * C::kTile) >> 4);
-            const bool free_k = ALT || t == 1 || j >= m1;
-            // the item's last score product with this Q
-            const bool free_q = !ALT ? j == (t == 0 ? m0 : m1) - 1 : t == 0 ? m0 == j + 1 && m1 <= j : m0 <= j + 1;
-            if (leader) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-                    mma_ss(tmem + t * 128, dq + off, dk + off, idesc_qk, kk > 0 ? 1u : 0u);
-                }
-                mma_commit(bar(C::bSFull + t));
-                if (free_k) mma_commit(bar(C::bKEmpty + s));
-                if (free_q) mma_commit(bar(C::bQEmpty + qi));
-            }
-            __syncwarp();
-            return true;
-        };
-        auto issue_pv = [&](auto T, int j) -> bool {
-            constexpr int t = decltype(T)::value;
-            const uint32_t tile = base + (ALT ? 2 * j + t : j);
-            const int s = tile % C::NV;
-            if (!warp_wait(bar(C::bVOk + s), (tile / C::NV) & 1)) return false;
-            if (j == 0) {
-                if (co[t] > 0 && !warp_wait(bar(C::bOFree + t), (co[t] - 1) & 1)) return false;
-                ++co[t];
-            }
-            const uint64_t dv = dv0 + static_cast<uint64_t>((s * C::kTile) >> 4);
-            const uint32_t par = cp[t] & 1;
-            ++cp[t];
-            const bool free_v = ALT || t == 1 || j >= n1;
-            const bool done = j == (t == 0 ? n0 : n1) - 1;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {   // P arrives in two halves of 64 keys
-                if (!warp_wait(bar((half ? C::bPFull : C::bPHalf) + t), par)) return false;
-                tc_fence_after();
-                if (leader) {
-#pragma unroll
-                    for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                        mma_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8, dv + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
-                               (j > 0 || kk > 0) ? 1u : 0u);
-                    if (half) {
-                        if (free_v) mma_commit(bar(C::bVEmpty + s));
-                        if (done) mma_commit(bar(C::bODone + t));
-                    }
-                }
-                __syncwarp();
-            }
-            return true;
-        };
-        const std::integral_constant<int, 0> t0;
-        const std::integral_constant<int, 1> t1;
-        uint32_t idx = 0;
-        bool s0 = false, s1 = false;   // first score products of the item already issued
         ok = warp_wait(item_bar(0), 0);
-        if (ok) read_item(0, &n0, &n1, &last);
+        if (ok) read_item(0, &n0, &n1, &last, &two);
+        uint32_t ahead = 0;                  // bit t: the first score product of this item's tile t is already issued
         while (ok && !last) {
-            if (!s0 && !issue_s(t0, base, 0, n0, n1, true)) break;
-            if (n1 > 0 && !s1 && !issue_s(t1, base, 0, n0, n1, true)) break;
-            s0 = s1 = false;
             const int most = max(n0, n1);
-            const uint32_t next = base + (ALT ? n0 + n1 : most);
+            const uint32_t next = base + (two ? n0 + n1 : most);
             int m0 = 0, m1 = 0, end = 1;
-            bool known = false;
-            for (int j = 0; j < most; ++j) {
-                const bool fin = j == most - 1;
-                if (fin) {
+            bool known = false, mtwo = ALT;
+            uint32_t early = 0;              // as `ahead`, for the next item
+#pragma unroll 1
+            for (int j = -1; j < most && ok; ++j) {
+                if (j == most - 1) {
                     known = __all_sync(0xffffffffu, mbar_try_wait(item_bar(idx + 1), ((idx + 1) / kItems) & 1));
-                    if (known) read_item(idx + 1, &m0, &m1, &end);
+                    if (known) read_item(idx + 1, &m0, &m1, &end, &mtwo);
                 }
-                if (j < n0) {
-                    if (!issue_pv(t0, j)) { ok = false; break; }
-                    if (j + 1 < n0 && !issue_s(t0, base, j + 1, n0, n1, true)) break;
+#pragma unroll 1
+                for (int t = 0; t < 2; ++t) {
+                    const int n = t == 0 ? n0 : n1;
+                    // ---- P V of key tile j
+                    if (j >= 0 && j < n) {
+                        const uint32_t tile = base + (two ? 2 * j + t : j);
+                        const uint32_t vs = tile % C::NV;
+                        if (!warp_wait(bar(C::bVOk + vs), (tile / C::NV) & 1)) { ok = false; break; }
+                        if (j == 0) {
+                            if ((begun >> t & 1) && !warp_wait(bar(C::bOFree + t), co >> t & 1)) { ok = false; break; }
+                            if (begun >> t & 1) co ^= 1u << t;
+                            begun |= 1u << t;
+                        }
+                        const uint64_t dv = dv0 + static_cast<uint64_t>((vs * C::kTile) >> 4);
+                        const uint32_t tO = tmem + 256 + t * D, tP = tmem + t * 128;
+                        if (!warp_wait(bar(C::bPFull + t), cp >> t & 1)) { ok = false; break; }
+                        cp ^= 1u << t;
+                        tc_fence_after();
+                        if (leader) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_ts(tO, tP + kk * 8, dv + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
+                                       (j > 0 || kk > 0) ? 1u : 0u);
+                            if (two || t == 1 || j >= n1) mma_commit(bar(C::bVEmpty + vs));
+                            if (j == n - 1) mma_commit(bar(C::bODone + t));
+                        }
+                        __syncwarp();
+                    }
+                    // ---- S of this tile's next key tile, here or (if all it needs is there) in the next item
+                    const bool here = j + 1 < n && !(j < 0 && (ahead >> t & 1));
+                    const bool there = j == most - 1 && known && !end && (t == 0 || (early & 1) != 0) && (t == 0 ? m0 : m1) > 0;
+                    if (!here && !there) continue;
+                    const int k = here ? j + 1 : 0, e0 = here ? n0 : m0, e1 = here ? n1 : m1;
+                    const bool turns = here ? two : mtwo;
+                    const uint32_t tile = (here ? base : next) + (turns ? 2 * k + t : k);
+                    const uint32_t ks = tile % C::NK, qi = ALT ? 0 : t;
+                    const uint32_t kb = bar(C::bKFull + ks), kpar = (tile / C::NK) & 1;
+                    const bool new_q = k == 0 && (!ALT || t == 0);
+                    if (here) {
+                        if (!warp_wait(kb, kpar) || (new_q && !warp_wait(bar(C::bQFull + qi), cq >> qi & 1))) { ok = false; break; }
+                    } else if (!__all_sync(0xffffffffu, mbar_try_wait(kb, kpar)) ||
+                               (new_q && !__all_sync(0xffffffffu, mbar_try_wait(bar(C::bQFull + qi), cq >> qi & 1)))) {
+                        continue;
+                    }
+                    if (new_q) cq ^= 1u << qi;
+                    if (!here) early |= 1u << t;
+                    tc_fence_after();
+                    const uint64_t dq = dq0 + static_cast<uint64_t>((qi * C::kTile) >> 4);
+                    const uint64_t dk = dk0 + static_cast<uint64_t>((ks * C::kTile) >> 4);
+                    const uint32_t tS = tmem + t * 128;
+                    // the item's last score product with this Q
+                    const bool free_q = !ALT ? k == (t == 0 ? e0 : e1) - 1 : t == 0 ? e0 == k + 1 && e1 <= k : e0 <= k + 1;
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+                            mma_ss(tS, dq + off, dk + off, idesc_qk, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit(bar(C::bSFull + t));
+                        if (turns || t == 1 || k >= e1) mma_commit(bar(C::bKEmpty + ks));
+                        if (free_q) mma_commit(bar(C::bQEmpty + qi));
+                    }
+                    __syncwarp();
                 }
-                if (fin && known && !end) s0 = issue_s(t0, next, 0, m0, m1, false);
-                if (j < n1) {
-                    if (!issue_pv(t1, j)) { ok = false; break; }
-                    if (j + 1 < n1 && !issue_s(t1, base, j + 1, n0, n1, true)) break;
-                }
-                if (s0 && m1 > 0) s1 = issue_s(t1, next, 0, m0, m1, false);
             }
             if (!ok) break;
             if (leader) mbar_arrive(bar(C::bItemEmpty + idx % kItems));
             ++idx;
             if (!known) {
                 if (!warp_wait(item_bar(idx), (idx / kItems) & 1)) { ok = false; break; }
-                read_item(idx, &m0, &m1, &end);
+                read_item(idx, &m0, &m1, &end, &mtwo);
             }
             base = next;
             n0 = m0;
             n1 = m1;
             last = end;
+            two = mtwo;
+            ahead = early;
         }
         if (!ok && leader) atomicOr(a.status, kStatusTimeout);
         if (leader) {
             mma_commit(bar(C::bDrain));   // every MMA issued so far completes before TMEM is released
             volatile int no_abort = 0;
-            mbar_wait(bar(C::bDrain), 0, &no_abort, 200000000ull);
+            mbar_wait_inl(bar(C::bDrain), 0, &no_abort, 200000000ull);
         }
         __syncwarp();
     } else if (warp < 4) {
         // ------------------------------------------------------------------ values of masked keys
+        setmaxnreg_dec<kRegsAux>();
         bool ok = true;
         uint32_t nv = 0;
         for (uint32_t i = 0; ok; ++i) {
             if (!warp_wait(item_bar(i), (i / kItems) & 1)) { ok = false; break; }
             Item *it = &items[i % kItems];
             if (it->last) break;
-            const int n = it->k1 - it->k0;
+            const bool duo = !TREE && it->duo;
+            const int n = duo ? it->n0 + it->n1 : it->k1 - it->k0;
             for (int j = 0; j < n; ++j, ++nv) {
                 const int s = nv % C::NV;
                 if (!warp_wait(bar(C::bVFull + s), (nv / C::NV) & 1)) { ok = false; break; }
-                if (it->k0 + j >= it->masked) {
+                if (it->k0 + (duo ? j >> 1 : j) >= it->masked) {
                     uint4 *tile = reinterpret_cast<uint4 *>(sm + C::kV + s * C::kTile);
                     bool odd = false;
 #pragma unroll 4
@@ -720,23 +705,25 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bItemEmpty + i % kItems));
         }
-    } else {
-        // ------------------------------------------------------------------ softmax and epilogue
+    } else if (warp < 12) {
+        // ------------------------------------------------------------------ softmax
+        setmaxnreg_inc<kRegsSoftmax>();
         const int t = (warp - 4) >> 2, q = warp & 3, r = q * 32 + lane;
         const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
         const uint32_t tS = trow + t * 128, tO = trow + 256 + t * D;
         const float c = a.scale * kLog2e;
         const uint64_t c2 = f2_pack(c, c);
-        const int my_tok = r / a.group, my_head = r - my_tok * a.group;   // within the tile
+        const int my_tok = r / a.group;   // within the tile
         float2 *stat = reinterpret_cast<float2 *>(sm + C::kStat);
-        uint32_t ns = 0, no = 0, no1 = 0;   // score tiles read, items finished (and of tile 1, seen from tile 0: ALT)
+        uint32_t ns = 0, no = 0;   // score tiles read, items finished
         bool ok = true;
         for (uint32_t i = 0; ok; ++i) {
             if (!warp_wait(item_bar(i), (i / kItems) & 1)) { ok = false; break; }
             const volatile Item *it = &items[i % kItems];
             if (it->last) break;
-            const int n = t == 0 ? it->n0 : it->n1, n1 = it->n1;
-            const int tok0 = it->tok0 + (ALT ? 0 : t * x.tpt);
+            const int n = t == 0 ? it->n0 : it->n1;
+            const bool duo = !TREE && it->duo;
+            const int tok0 = it->tok0 + (ALT || duo ? 0 : t * x.tpt);
             const int rows = min(x.tpt, it->tokens - tok0) * a.group;
             const bool mine = r < rows;
             const bool active = q * 32 < rows;      // some row of the warp
@@ -750,38 +737,38 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                 tc_fence_after();
                 if (active) {
                     const int kt = k0 + (ALT ? 2 * j + t : j);
-                    uint32_t s[4][32];
-                    float top[4];
-                    const bool hide = kt >= masked;
+                    uint64_t sum = f2_pack(0.f, 0.f), sum2 = sum;
+                    // maximum of 32 scores; 2^(c s - m) of 32 scores, to P
+                    auto maximum = [&](const uint32_t (&s)[32]) -> float {
+                        float u[4];
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) tmem_ld32(tS + h * 32, s[h]);
-                    tmem_ld_wait();
-                    if (hide) {
+                        for (int e = 0; e < 4; ++e) u[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const int first = kt * 128 + h * 32;
-                            const uint32_t seen = TREE ? seen_tree(bits, len, first) : seen_causal(tok, first);
+                        for (int e = 8; e < 32; e += 2)
+                            u[e >> 1 & 3] = fmax3(u[e >> 1 & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                        return fmaxf(fmax3(u[0], u[1], u[2]), u[3]);
+                    };
+                    auto exponentials = [&](int h, const uint32_t (&s)[32], uint64_t off) {
+                        uint32_t pk[16];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(seen >> e & 1u)) s[h][e] = 0xff800000u;
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 y = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, off));
+                            const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+                            if (e & 1) sum = f2_add(sum, f2_pack(p0, p1));
+                            else sum2 = f2_add(sum2, f2_pack(p0, p1));
+                            pk[e] = pack_bf16x2(p0, p1);
                         }
-                    }
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        top[h] = fmaxf(__uint_as_float(s[h][0]), __uint_as_float(s[h][1]));
-#pragma unroll
-                        for (int e = 2; e < 32; e += 2)
-                            top[h] = fmax3(top[h], __uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]));
-                    }
-                    const float mx = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * c;
-                    const bool grow = mx > m + kGrow;
-                    if (__any_sync(0xffffffffu, grow)) {
+                        tmem_st16(tS + h * 16, pk);   // over scores that have been read
+                    };
+                    auto rescale = [&](float mx) {
+                        const bool grow = mx > m + kGrow;
+                        if (!__any_sync(0xffffffffu, grow)) return;
                         const float to = grow ? mx : m;
                         const float alpha = grow ? ex2_approx(m - to) : 1.0f;
                         l *= alpha;
                         m = to;
                         if (j > 0) {   // P V of the tiles before is complete: S of this one came behind it
-#pragma unroll
+#pragma unroll 1
                             for (int h = 0; h < D / 16; ++h) {
                                 uint32_t o[16];
                                 tmem_ld16(tO + h * 16, o);
@@ -791,170 +778,250 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                                 tmem_st16(tO + h * 16, o);
                             }
                         }
-                    }
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    const uint64_t off = f2_pack(-ref, -ref);
-                    uint64_t sum = f2_pack(0.f, 0.f), sum2 = sum;
-                    auto exponentials = [&](auto poly) {
+                    };
+                    if (!ALT && kt < masked) {
+                        // all scores at once in registers
+                        uint32_t s[4][32];
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) tmem_ld32(tS + h * 32, s[h]);
+                        tmem_ld_wait();
+                        rescale(fmaxf(fmax3(maximum(s[0]), maximum(s[1]), maximum(s[2])), maximum(s[3])) * c);
+                        const float ref = m == -INFINITY ? 0.f : m;
+                        const uint64_t off = f2_pack(-ref, -ref);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) exponentials(h, s[h], off);
+                    } else {
+                        // 32 at a time, twice: short code for the instruction cache, and 32 keys that no row of the warp
+                        // sees are passed over
+                        uint32_t seen[4];
+                        int kind = 0;   // bits 2h, 2h + 1: none of the warp's rows sees any of the 32; some row not all
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[h][2 * e]), __uint_as_float(s[h][2 * e + 1])), c2, off);
-                                uint64_t pr;
-                                if (decltype(poly)::value && e % kPolyEvery == kPolyEvery - 1) {
-                                    pr = exp2_poly(y);
-                                } else {
-                                    const float2 z = f2_unpack(y);
-                                    pr = f2_pack(ex2_approx(z.x), ex2_approx(z.y));
-                                }
-                                if (e & 1) sum = f2_add(sum, pr);
-                                else sum2 = f2_add(sum2, pr);
-                                const float2 z = f2_unpack(pr);
-                                pk[e] = pack_bf16x2(z.x, z.y);
-                            }
-                            tmem_st16(tS + h * 16, pk);
-                            if (h == 1) {
-                                tmem_st_wait();
-                                tc_fence_before();
-                                warp_arrive(bar(C::bPHalf + t));
-                            }
+                            const int first = kt * 128 + h * 32;
+                            seen[h] = kt < masked ? 0xffffffffu : TREE ? seen_tree(bits, len, first) : seen_causal(tok, first);
+                            const bool none = __all_sync(0xffffffffu, seen[h] == 0u), all = __all_sync(0xffffffffu, seen[h] == 0xffffffffu);
+                            kind |= (none ? 1 : all ? 0 : 2) << (2 * h);
                         }
-                    };
-                    // masked scores (-inf) must give exact zeros, which the polynomial does not
-                    if (hide || __any_sync(0xffffffffu, mx == -INFINITY)) exponentials(std::false_type());
-                    else exponentials(std::true_type());
+                        auto read = [&](int h, uint32_t (&s)[32]) {
+                            tmem_ld32(tS + h * 32, s);
+                            tmem_ld_wait();
+                            if (kind >> (2 * h) & 2) {
+                                const uint32_t w = h == 0 ? seen[0] : h == 1 ? seen[1] : h == 2 ? seen[2] : seen[3];
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(w >> e & 1u)) s[e] = 0xff800000u;
+                            }
+                        };
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int h = 0; h < 4; ++h) {
+                            if (kind >> (2 * h) & 1) continue;
+                            uint32_t s[32];
+                            read(h, s);
+                            top = fmaxf(top, maximum(s));
+                        }
+                        rescale(top * c);
+                        const float ref = m == -INFINITY ? 0.f : m;
+                        const uint64_t off = f2_pack(-ref, -ref);
+#pragma unroll 1
+                        for (int h = 0; h < 4; ++h) {
+                            if (kind >> (2 * h) & 1) {
+                                uint32_t zero[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) zero[e] = 0u;
+                                tmem_st16(tS + h * 16, zero);
+                                continue;
+                            }
+                            uint32_t s[32];
+                            read(h, s);
+                            exponentials(h, s, off);
+                        }
+                    }
                     const float2 both = f2_unpack(f2_add(sum, sum2));
                     l += both.x + both.y;
                     tmem_st_wait();
-                } else {
-                    warp_arrive(bar(C::bPHalf + t));
                 }
                 tc_fence_before();
                 warp_arrive(bar(C::bPFull + t));
             }
             if (!ok) break;
-            // ---- epilogue
-            float w0 = 1.f, w1 = 0.f;
-            if (ALT && t == 1) {
-                if (n > 0) {
-                    // this item's first P V waited until tile 0 had read the previous item's O and statistics
-                    if (!warp_wait(bar(C::bODone + 1), no & 1)) { ok = false; break; }
-                    ++no;
-                    stat[r] = make_float2(m, l);
-                    warp_arrive(bar(C::bStat));
-                }
-            } else if (n > 0) {
-                if (!warp_wait(bar(C::bODone + t), no & 1)) { ok = false; break; }
+            if (n > 0) {
+                // the epilogue warps take it from here, while this warp begins the next item
+                if (no > 0 && !warp_wait(bar(C::bStatFree + t), (no - 1) & 1)) { ok = false; break; }
                 ++no;
-                if (ALT && n1 > 0) {
-                    if (!warp_wait(bar(C::bStat), no1 & 1) || !warp_wait(bar(C::bODone + 1), no1 & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    ++no1;
-                    const float2 other = stat[r];
+                stat[t * 128 + r] = make_float2(m, l);
+                warp_arrive(bar(C::bStat + t));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::bItemEmpty + i % kItems));
+        }
+        if (!ok) atomicOr(a.status, kStatusTimeout);
+    } else {
+        // ------------------------------------------------------------------ epilogue
+        setmaxnreg_dec<kRegsOut>();
+        const int q = warp & 3, r = q * 32 + lane;
+        const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        const int my_tok = r / a.group, my_head = r - my_tok * a.group;   // within the tile
+        const float2 *stat = reinterpret_cast<const float2 *>(sm + C::kStat);
+        unsigned char *stage = sm + C::kOut + q * 4096;
+        constexpr int kPartRows = ALT ? 128 : 256;
+        uint32_t done = 0;   // parities, bit t: items of tile t
+        bool ok = true;
+        for (uint32_t i = 0; ok; ++i) {
+            if (!warp_wait(item_bar(i), (i / kItems) & 1)) { ok = false; break; }
+            const volatile Item *it = &items[i % kItems];
+            if (it->last) break;
+            const bool join = ALT && it->n1 > 0, duo = !TREE && it->duo;
+#pragma unroll 1
+            for (int t = 0; t < C::NQ; ++t) {
+                if ((t == 0 ? it->n0 : it->n1) == 0) continue;
+                if (!warp_wait(bar(C::bStat + t), done >> t & 1) || !warp_wait(bar(C::bODone + t), done >> t & 1)) { ok = false; break; }
+                done ^= 1u << t;
+                const float2 st = stat[t * 128 + r];
+                float m = st.x, l = st.y, w0 = 1.f, w1 = 0.f;
+                if (join) {
+                    if (!warp_wait(bar(C::bStat + 1), done >> 1 & 1) || !warp_wait(bar(C::bODone + 1), done >> 1 & 1)) { ok = false; break; }
+                    done ^= 2u;
+                    const float2 other = stat[128 + r];
                     const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
                     w0 = ex2_approx(m - ref);
                     w1 = ex2_approx(other.x - ref);
                     l = w0 * l + w1 * other.y;
                     m = top;
+                    warp_arrive(bar(C::bStatFree + 1));
                 }
+                warp_arrive(bar(C::bStatFree + t));
                 tc_fence_after();
-                const int slot = it->slot;
+                const int tok0 = it->tok0 + (ALT || duo ? 0 : t * x.tpt);
+                const int rows = min(x.tpt, it->tokens - tok0) * a.group;
+                const bool mine = r < rows, active = q * 32 < rows;
+                const int tok = tok0 + my_tok;
+                const int slot = it->slot, len = it->len;
                 const bool odd = it->odd != 0;
-                const bool join = ALT && n1 > 0;
-                const int head = it->kh * a.group + my_head;
+                const int kh = it->kh + (duo ? t : 0), head = kh * a.group + my_head;
                 const int64_t row = it->start + tok;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
+                const uint32_t tO = trow + 256 + t * D;
                 float *part = nullptr;
-                if (TREE && slot >= 0)
-                    part = tree_slot(a.ws, gridDim.x, slot, ALT ? 128 : 256, D);
+                if (TREE && slot >= 0) part = tree_slot(a.ws, gridDim.x, slot, kPartRows, D);
                 const int prow = r + (ALT ? 0 : t * x.tpt * a.group);   // row within the segment
-                if (active) {
-#pragma unroll 1
-                    for (int h = 0; h < D / 32; ++h) {
-                        __syncwarp();
-                        uint32_t o[32];
-                        tmem_ld32(tO + h * 32, o);
-                        tmem_ld_wait();
-                        if (join) {
-                            uint32_t o1[32];
-                            tmem_ld32(trow + 256 + D + h * 32, o1);
+                const int64_t out_at = mine ? row * a.o_tok + static_cast<int64_t>(head) * a.o_head : -1;
+
+                // 32 columns of O (of both tiles: ALT), with the values that were replaced by 0 for the rows that see them
+                auto read = [&](int h, uint32_t (&o)[32]) {
+                    __syncwarp();
+                    tmem_ld32(tO + h * 32, o);
+                    tmem_ld_wait();
+                    if (join) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t o1[16];
+                            tmem_ld16(tO + D + h * 32 + g * 16, o1);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(w0 * __uint_as_float(o[e]) + w1 * __uint_as_float(o1[e]));
+                            for (int e = 0; e < 16; ++e)
+                                o[g * 16 + e] = __float_as_uint(w0 * __uint_as_float(o[g * 16 + e]) + w1 * __uint_as_float(o1[e]));
                         }
-                        if (odd && mine) {
-                            // values that were replaced by 0: the rows that see them get them now
-                            const int end = min(it->len + it->tokens, it->k1 * 128);
-                            for (int key = max(it->masked, it->k0) * 128; key < end; ++key) {
-                                const bool sees = TREE ? seen_tree(bits, len, key) & 1u : key <= tok;
-                                if (!sees) continue;
-                                const uint16_t *v;
-                                if (TREE) {
-                                    const int id = a.table[it->kv + (key >> a.page_shift)];
-                                    if (id < 0 || id >= a.pages) continue;
-                                    v = static_cast<const uint16_t *>(a.vp) +
-                                        (((static_cast<int64_t>(id) * a.kv_heads + it->kh) << a.page_shift) +
-                                         (key & ((1 << a.page_shift) - 1))) * D;
-                                } else {
-                                    v = static_cast<const uint16_t *>(a.v) + (it->kv + key) * a.v_tok + it->kh * a.v_head;
-                                }
+                    }
+                    if (odd && mine) {
+                        const uint64_t bits = TREE ? tree_bits(a, it->start, tok, it->tokens) : 0;
+                        const int end = min(len + it->tokens, it->k1 * 128);
+                        for (int key = max(it->masked, it->k0) * 128; key < end; ++key) {
+                            const bool sees = TREE ? seen_tree(bits, len, key) & 1u : key <= tok;
+                            if (!sees) continue;
+                            const uint16_t *v;
+                            if (TREE) {
+                                const int id = a.table[it->kv + (key >> a.page_shift)];
+                                if (id < 0 || id >= a.pages) continue;
+                                v = static_cast<const uint16_t *>(a.vp) +
+                                    (((static_cast<int64_t>(id) * a.kv_heads + kh) << a.page_shift) +
+                                     (key & ((1 << a.page_shift) - 1))) * D;
+                            } else {
+                                v = static_cast<const uint16_t *>(a.v) + (it->kv + key) * a.v_tok + kh * a.v_head;
+                            }
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const float f = bf16_bits_to_float(v[h * 32 + e]);
-                                    if (!(fabsf(f) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
-                                }
+                            for (int e = 0; e < 32; ++e) {
+                                const float f = bf16_bits_to_float(v[h * 32 + e]);
+                                if (!(fabsf(f) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
                             }
                         }
-                        if (!mine) continue;
-                        if (TREE && part) {
-                            float4 *dst = reinterpret_cast<float4 *>(part + prow * D + h * 32);
+                    }
+                    if (!part && l == 0.f) {   // a row that sees nothing
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    }
+                    __syncwarp();
+                };
+                auto free_o = [&]() {
+                    tc_fence_before();
+                    warp_arrive(bar(C::bOFree + t));
+                    if (join) warp_arrive(bar(C::bOFree + 1));
+                };
+                if (!active) {
+                    free_o();
+                } else if (!part && a.out_dtype == 0) {
+                    // 64 columns of O / l at a time in bf16
+#pragma unroll 1
+                    for (int h = 0; h < D / 64; ++h) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t o[32];
+                            read(2 * h + g, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                w[g * 16 + e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                        }
+                        if (h == D / 64 - 1) free_o();
+                        if (!ALT) {
+                            // through shared memory: a thread has a row, but a warp's store should cover whole 128-byte pieces
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                     __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-                            continue;
-                        }
-                        const int64_t at = row * a.o_tok + static_cast<int64_t>(head) * a.o_head + h * 32;
-                        if (a.out_dtype == 0) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int f = 0; f < 4; ++f)
-                                    w[f] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[8 * e + 2 * f]) * inv,
-                                                                       __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
-                                dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        } else {
-                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at);
+                                *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                                    make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                            __syncwarp();
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                float w[4];
-#pragma unroll
-                                for (int f = 0; f < 4; ++f) w[f] = l == 0.f ? 0.f : __uint_as_float(o[4 * e + f]) * inv;
-                                dst[e] = make_float4(w[0], w[1], w[2], w[3]);
+                                const int rr = e * 4 + (lane >> 3), ch = lane & 7;
+                                const int64_t to = __shfl_sync(0xffffffffu, out_at, rr);
+                                const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+                                if (to >= 0) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + to + h * 64 + ch * 8) = v;
                             }
+                            __syncwarp();
+                        } else if (mine) {
+                            // few rows: straight from the threads
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + out_at + h * 64);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                         }
                     }
-                    if (mine) {
-                        if (TREE && part) {
-                            const int pr = ALT ? 128 : 256;
-                            part[pr * D + prow] = m;
-                            part[pr * (D + 1) + prow] = l;
-                        } else if (a.lse) {
-                            a.lse[static_cast<int64_t>(head) * a.tokens + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                } else {
+                    // fp32 rows: of the output, or of a piece's numerators
+                    float *dst = part ? part + static_cast<int64_t>(prow) * D : static_cast<float *>(a.o) + out_at;
+                    const float f = part ? 1.f : inv;
+#pragma unroll 1
+                    for (int h = 0; h < D / 32; ++h) {
+                        uint32_t o[32];
+                        read(h, o);
+                        if (mine) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                reinterpret_cast<float4 *>(dst + h * 32)[e] =
+                                    make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                                __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
                         }
+                    }
+                    __syncwarp();
+                    free_o();
+                }
+                if (mine) {
+                    if (part) {
+                        part[kPartRows * D + prow] = m;
+                        part[kPartRows * (D + 1) + prow] = l;
+                    } else if (a.lse) {
+                        a.lse[static_cast<int64_t>(head) * a.tokens + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                     }
                 }
-                tc_fence_before();
-                warp_arrive(bar(C::bOFree + t));
-                if (join) warp_arrive(bar(C::bOFree + 1));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bItemEmpty + i % kItems));
