@@ -46,7 +46,7 @@ using namespace sm100;
 constexpr int kThreads = 512;
 // Registers per thread of the four warpgroups after the start (512 threads start with 128 each): loads, MMAs and checks;
 // softmax (two); epilogue.
-constexpr int kRegsAux = 80, kRegsSoftmax = 168, kRegsOut = 96;
+constexpr int kRegsAux = 64, kRegsSoftmax = 168, kRegsOut = 112;
 static_assert(kRegsAux + 2 * kRegsSoftmax + kRegsOut <= 512, "the shares add up to what the block starts with");
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -107,6 +107,23 @@ struct TcArgs {
     int box_rows;    // rows that a Q load brings
     int plan;        // prompt: items come from the list in the workspace
 };
+
+// Wait for a phase of a barrier, at most about 2 s of global time. Inlined in few instructions: under a register split no
+// function can be called, and code that runs once per item is mostly waited for by instruction fetches.
+__device__ __forceinline__ uint32_t timer_lo() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t limit_ns = 2000000000u) {
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+    const uint32_t t0 = timer_lo();
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+    } while (*abort == 0 && timer_lo() - t0 < limit_ns);
+    *abort = 1;
+    return false;
+}
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z) {
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
@@ -297,6 +314,12 @@ __device__ __forceinline__ uint32_t seen_tree(uint64_t bits, int len, int first)
     return static_cast<uint32_t>(bits << -s) | ((1u << -s) - 1u);
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -367,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
     grid_dependency_wait();   // the list of prompt items, if a kernel in front of this one makes it
 
     // a wait of a whole warp: all of its lanes go on or none
-    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait_inl(b, parity, abort_flag)); };
+    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, bar_wait(b, parity, abort_flag)); };
     // the item ring, read by all roles but the loader
     // one arrival for a warp whose lanes have all got here (and fenced what they wrote)
     auto warp_arrive = [&](uint32_t b) {
@@ -528,11 +551,11 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
             // the copies in flight land before the block ends
             volatile int no_abort = 0;
             for (uint32_t i = nk > C::NK ? nk - C::NK : 0; i < nk; ++i)
-                mbar_wait_inl(bar(C::bKFull + i % C::NK), (i / C::NK) & 1, &no_abort, 200000000ull);
+                bar_wait(bar(C::bKFull + i % C::NK), (i / C::NK) & 1, &no_abort, 200000000u);
             for (uint32_t i = nv > C::NV ? nv - C::NV : 0; i < nv; ++i)
-                mbar_wait_inl(bar(C::bVFull + i % C::NV), (i / C::NV) & 1, &no_abort, 200000000ull);
+                bar_wait(bar(C::bVFull + i % C::NV), (i / C::NV) & 1, &no_abort, 200000000u);
             for (int t = 0; t < C::NQ; ++t)
-                if (nq[t]) mbar_wait_inl(bar(C::bQFull + t), (nq[t] - 1) & 1, &no_abort, 200000000ull);
+                if (nq[t]) bar_wait(bar(C::bQFull + t), (nq[t] - 1) & 1, &no_abort, 200000000u);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
@@ -658,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
         if (leader) {
             mma_commit(bar(C::bDrain));   // every MMA issued so far completes before TMEM is released
             volatile int no_abort = 0;
-            mbar_wait_inl(bar(C::bDrain), 0, &no_abort, 200000000ull);
+            bar_wait(bar(C::bDrain), 0, &no_abort, 200000000u);
         }
         __syncwarp();
     } else if (warp < 4) {
@@ -779,8 +802,26 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                             }
                         }
                     };
+                    auto seen_of = [&](int h) -> uint32_t {
+                        const int first = kt * 128 + h * 32;
+                        return TREE ? seen_tree(bits, len, first) : seen_causal(tok, first);
+                    };
+                    auto conceal = [&](uint32_t w, uint32_t (&s)[32]) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(w >> e & 1u)) s[e] = 0xff800000u;
+                    };
+                    // The quarters of the tile in front of `quarters` hold every key that some row of the warp sees.
+                    int quarters = 4;
+                    if (!ALT && kt >= masked) {
+#pragma unroll
+                        for (int h = 3; h >= 0; --h)
+                            if (quarters == h + 1 && __all_sync(0xffffffffu, seen_of(h) == 0u)) quarters = h;
+                    }
                     if (!ALT && kt < masked) {
-                        // all scores at once in registers
+                        // A tile that all rows see: its scores at once in registers, in one piece of straight code. Branches in it,
+                        // for masks too, cost more in lost overlap than they save (2.15 against 1.83 ms for 32768 tokens with
+                        // masks and skipped quarters here).
                         uint32_t s[4][32];
 #pragma unroll
                         for (int h = 0; h < 4; ++h) tmem_ld32(tS + h * 32, s[h]);
@@ -791,31 +832,19 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
 #pragma unroll
                         for (int h = 0; h < 4; ++h) exponentials(h, s[h], off);
                     } else {
-                        // 32 at a time, twice: short code for the instruction cache, and 32 keys that no row of the warp
-                        // sees are passed over
-                        uint32_t seen[4];
-                        int kind = 0;   // bits 2h, 2h + 1: none of the warp's rows sees any of the 32; some row not all
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const int first = kt * 128 + h * 32;
-                            seen[h] = kt < masked ? 0xffffffffu : TREE ? seen_tree(bits, len, first) : seen_causal(tok, first);
-                            const bool none = __all_sync(0xffffffffu, seen[h] == 0u), all = __all_sync(0xffffffffu, seen[h] == 0xffffffffu);
-                            kind |= (none ? 1 : all ? 0 : 2) << (2 * h);
-                        }
+                        // Diagonal tiles, and ALT, which waits for memory: 32 scores at a time, twice, without the quarters that
+                        // no row sees (256 short prompts: 88 -> 69 us)
                         auto read = [&](int h, uint32_t (&s)[32]) {
                             tmem_ld32(tS + h * 32, s);
                             tmem_ld_wait();
-                            if (kind >> (2 * h) & 2) {
-                                const uint32_t w = h == 0 ? seen[0] : h == 1 ? seen[1] : h == 2 ? seen[2] : seen[3];
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!(w >> e & 1u)) s[e] = 0xff800000u;
+                            if (kt >= masked) {
+                                const uint32_t w = seen_of(h);
+                                if (!__all_sync(0xffffffffu, w == 0xffffffffu)) conceal(w, s);
                             }
                         };
                         float top = -INFINITY;
 #pragma unroll 1
-                        for (int h = 0; h < 4; ++h) {
-                            if (kind >> (2 * h) & 1) continue;
+                        for (int h = 0; h < quarters; ++h) {
                             uint32_t s[32];
                             read(h, s);
                             top = fmaxf(top, maximum(s));
@@ -824,17 +853,17 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                         const float ref = m == -INFINITY ? 0.f : m;
                         const uint64_t off = f2_pack(-ref, -ref);
 #pragma unroll 1
-                        for (int h = 0; h < 4; ++h) {
-                            if (kind >> (2 * h) & 1) {
-                                uint32_t zero[16];
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) zero[e] = 0u;
-                                tmem_st16(tS + h * 16, zero);
-                                continue;
-                            }
+                        for (int h = 0; h < quarters; ++h) {
                             uint32_t s[32];
                             read(h, s);
                             exponentials(h, s, off);
+                        }
+                        if (!ALT) {
+                            uint32_t zero[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) zero[e] = 0u;
+#pragma unroll 1
+                            for (int h = quarters; h < 4; ++h) tmem_st16(tS + h * 16, zero);
                         }
                     }
                     const float2 both = f2_unpack(f2_add(sum, sum2));
@@ -862,6 +891,14 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
         const int q = warp & 3, r = q * 32 + lane;
         const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
         const int my_tok = r / a.group, my_head = r - my_tok * a.group;   // within the tile
+        const int64_t my_off = my_tok * a.o_tok + my_head * a.o_head;
+        // the 16-byte pieces that this thread stores of the warp's 32 rows: piece lane % 8 of rows 4 e + lane / 8
+        int64_t piece[ALT ? 1 : 8];
+#pragma unroll
+        for (int e = 0; e < 8 && !ALT; ++e) {
+            const int rr = q * 32 + e * 4 + (lane >> 3), tk = rr / a.group;
+            piece[ALT ? 0 : e] = tk * a.o_tok + (rr - tk * a.group) * a.o_head + (lane & 7) * 8;
+        }
         const float2 *stat = reinterpret_cast<const float2 *>(sm + C::kStat);
         unsigned char *stage = sm + C::kOut + q * 4096;
         constexpr int kPartRows = ALT ? 128 : 256;
@@ -869,45 +906,46 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
         bool ok = true;
         for (uint32_t i = 0; ok; ++i) {
             if (!warp_wait(item_bar(i), (i / kItems) & 1)) { ok = false; break; }
-            const volatile Item *it = &items[i % kItems];
-            if (it->last) break;
-            const bool join = ALT && it->n1 > 0, duo = !TREE && it->duo;
+            Item *const at = &items[i % kItems];
+            const Item &it = *at;
+            if (it.last) break;
+            const bool join = ALT && it.n1 > 0, duo = !TREE && it.duo;
 #pragma unroll 1
             for (int t = 0; t < C::NQ; ++t) {
-                if ((t == 0 ? it->n0 : it->n1) == 0) continue;
-                if (!warp_wait(bar(C::bStat + t), done >> t & 1) || !warp_wait(bar(C::bODone + t), done >> t & 1)) { ok = false; break; }
-                done ^= 1u << t;
+                if ((t == 0 ? it.n0 : it.n1) == 0) continue;
+                // everything that does not depend on the result comes before the wait for it
+                const int tok0 = it.tok0 + (ALT || duo ? 0 : t * x.tpt);
+                const int rows = min(x.tpt, it.tokens - tok0) * a.group;
+                const bool mine = r < rows, active = q * 32 < rows;
+                const int tok = tok0 + my_tok;
+                const int kh = it.kh + (duo ? t : 0);
+                const int64_t tile_off = (static_cast<int64_t>(it.start) + tok0) * a.o_tok + static_cast<int64_t>(kh) * a.group * a.o_head;
+                const uint32_t tO = trow + 256 + t * D;
+                float *part = nullptr;
+                if (TREE && it.slot >= 0) part = tree_slot(a.ws, gridDim.x, it.slot, kPartRows, D);
+                const int prow = r + (ALT ? 0 : t * x.tpt * a.group);   // row within the segment
+                if (!warp_wait(bar(C::bStat + t), done >> t & 1)) { ok = false; break; }
                 const float2 st = stat[t * 128 + r];
                 float m = st.x, l = st.y, w0 = 1.f, w1 = 0.f;
+                warp_arrive(bar(C::bStatFree + t));
                 if (join) {
-                    if (!warp_wait(bar(C::bStat + 1), done >> 1 & 1) || !warp_wait(bar(C::bODone + 1), done >> 1 & 1)) { ok = false; break; }
-                    done ^= 2u;
+                    if (!warp_wait(bar(C::bStat + 1), done >> 1 & 1)) { ok = false; break; }
                     const float2 other = stat[128 + r];
+                    warp_arrive(bar(C::bStatFree + 1));
                     const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
                     w0 = ex2_approx(m - ref);
                     w1 = ex2_approx(other.x - ref);
                     l = w0 * l + w1 * other.y;
                     m = top;
-                    warp_arrive(bar(C::bStatFree + 1));
+                    if (!warp_wait(bar(C::bODone + 1), done >> 1 & 1)) { ok = false; break; }
+                    done ^= 2u;
                 }
-                warp_arrive(bar(C::bStatFree + t));
+                const float inv = l == 0.f ? 0.f : rcp_approx(l);
+                if (!warp_wait(bar(C::bODone + t), done >> t & 1)) { ok = false; break; }
+                done ^= 1u << t;
                 tc_fence_after();
-                const int tok0 = it->tok0 + (ALT || duo ? 0 : t * x.tpt);
-                const int rows = min(x.tpt, it->tokens - tok0) * a.group;
-                const bool mine = r < rows, active = q * 32 < rows;
-                const int tok = tok0 + my_tok;
-                const int slot = it->slot, len = it->len;
-                const bool odd = it->odd != 0;
-                const int kh = it->kh + (duo ? t : 0), head = kh * a.group + my_head;
-                const int64_t row = it->start + tok;
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                const uint32_t tO = trow + 256 + t * D;
-                float *part = nullptr;
-                if (TREE && slot >= 0) part = tree_slot(a.ws, gridDim.x, slot, kPartRows, D);
-                const int prow = r + (ALT ? 0 : t * x.tpt * a.group);   // row within the segment
-                const int64_t out_at = mine ? row * a.o_tok + static_cast<int64_t>(head) * a.o_head : -1;
 
-                // 32 columns of O (of both tiles: ALT), with the values that were replaced by 0 for the rows that see them
+                // 32 columns of O (of both tiles: ALT)
                 auto read = [&](int h, uint32_t (&o)[32]) {
                     __syncwarp();
                     tmem_ld32(tO + h * 32, o);
@@ -923,33 +961,6 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                                 o[g * 16 + e] = __float_as_uint(w0 * __uint_as_float(o[g * 16 + e]) + w1 * __uint_as_float(o1[e]));
                         }
                     }
-                    if (odd && mine) {
-                        const uint64_t bits = TREE ? tree_bits(a, it->start, tok, it->tokens) : 0;
-                        const int end = min(len + it->tokens, it->k1 * 128);
-                        for (int key = max(it->masked, it->k0) * 128; key < end; ++key) {
-                            const bool sees = TREE ? seen_tree(bits, len, key) & 1u : key <= tok;
-                            if (!sees) continue;
-                            const uint16_t *v;
-                            if (TREE) {
-                                const int id = a.table[it->kv + (key >> a.page_shift)];
-                                if (id < 0 || id >= a.pages) continue;
-                                v = static_cast<const uint16_t *>(a.vp) +
-                                    (((static_cast<int64_t>(id) * a.kv_heads + kh) << a.page_shift) +
-                                     (key & ((1 << a.page_shift) - 1))) * D;
-                            } else {
-                                v = static_cast<const uint16_t *>(a.v) + (it->kv + key) * a.v_tok + kh * a.v_head;
-                            }
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float f = bf16_bits_to_float(v[h * 32 + e]);
-                                if (!(fabsf(f) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
-                            }
-                        }
-                    }
-                    if (!part && l == 0.f) {   // a row that sees nothing
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0u;
-                    }
                     __syncwarp();
                 };
                 auto free_o = [&]() {
@@ -961,6 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                     free_o();
                 } else if (!part && a.out_dtype == 0) {
                     // 64 columns of O / l at a time in bf16
+                    __nv_bfloat16 *const tile_out = static_cast<__nv_bfloat16 *>(a.o) + tile_off;
 #pragma unroll 1
                     for (int h = 0; h < D / 64; ++h) {
                         uint32_t w[32];
@@ -980,24 +992,27 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                                 *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
                                     make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                             __syncwarp();
+                            uint4 v[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                const int rr = e * 4 + (lane >> 3), ch = lane & 7;
-                                const int64_t to = __shfl_sync(0xffffffffu, out_at, rr);
-                                const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
-                                if (to >= 0) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + to + h * 64 + ch * 8) = v;
+                                const int rr = e * 4 + (lane >> 3);
+                                v[e] = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
                             }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (q * 32 + e * 4 + (lane >> 3) < rows)
+                                    *reinterpret_cast<uint4 *>(tile_out + piece[ALT ? 0 : e] + h * 64) = v[e];
                             __syncwarp();
                         } else if (mine) {
                             // few rows: straight from the threads
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + out_at + h * 64);
+                            uint4 *dst = reinterpret_cast<uint4 *>(tile_out + my_off + h * 64);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                         }
                     }
                 } else {
                     // fp32 rows: of the output, or of a piece's numerators
-                    float *dst = part ? part + static_cast<int64_t>(prow) * D : static_cast<float *>(a.o) + out_at;
+                    float *dst = part ? part + static_cast<int64_t>(prow) * D : static_cast<float *>(a.o) + tile_off + my_off;
                     const float f = part ? 1.f : inv;
 #pragma unroll 1
                     for (int h = 0; h < D / 32; ++h) {
@@ -1014,12 +1029,47 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                     __syncwarp();
                     free_o();
                 }
+                const int64_t out_at = tile_off + my_off;
+                const bool odd = *const_cast<const volatile int *>(&at->odd) != 0;
+                __syncwarp();
+                if (odd && mine) {
+                    // values that were replaced by 0: added to what the rows that see them have just been given
+                    const uint64_t bits = TREE ? tree_bits(a, it.start, tok, it.tokens) : 0;
+                    const int end = min(it.len + it.tokens, it.k1 * 128);
+                    for (int key = max(it.masked, it.k0) * 128; key < end; ++key) {
+                        const bool sees = TREE ? seen_tree(bits, it.len, key) & 1u : key <= tok;
+                        if (!sees) continue;
+                        const uint16_t *v;
+                        if (TREE) {
+                            const int id = a.table[it.kv + (key >> a.page_shift)];
+                            if (id < 0 || id >= a.pages) continue;
+                            v = static_cast<const uint16_t *>(a.vp) +
+                                (((static_cast<int64_t>(id) * a.kv_heads + kh) << a.page_shift) +
+                                 (key & ((1 << a.page_shift) - 1))) * D;
+                        } else {
+                            v = static_cast<const uint16_t *>(a.v) + (it.kv + key) * a.v_tok + kh * a.v_head;
+                        }
+#pragma unroll 1
+                        for (int e = 0; e < D; ++e) {
+                            const float f = bf16_bits_to_float(v[e]);
+                            if (fabsf(f) < INFINITY) continue;
+                            if (part) {
+                                part[prow * D + e] += f;
+                            } else if (a.out_dtype == 0) {
+                                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.o) + out_at + e;
+                                *dst = __float2bfloat16_rn(__bfloat162float(*dst) + f);
+                            } else {
+                                static_cast<float *>(a.o)[out_at + e] += f;
+                            }
+                        }
+                    }
+                }
                 if (mine) {
                     if (part) {
                         part[kPartRows * D + prow] = m;
                         part[kPartRows * (D + 1) + prow] = l;
                     } else if (a.lse) {
-                        a.lse[static_cast<int64_t>(head) * a.tokens + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                        a.lse[(static_cast<int64_t>(kh) * a.group + my_head) * a.tokens + it.start + tok] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                     }
                 }
             }

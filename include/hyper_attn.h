@@ -305,8 +305,8 @@ HA_API int hyper_attn_forward_noalloc(const void *Q, const void *K, const void *
  *   - Offsets, lengths, slots, masks and page tables are device memory and are read when the kernels run. An
  *     entry out of range leaves its sequence out (nothing of it is written) and makes hyper_attn_status report
  *     HA_ERR_INVALID_ARG; nothing is read or written out of bounds.
- *   - A row whose scores are all masked or -inf gives O = 0 and a log normaliser of -inf. Infinities and NaN
- *     in keys and values that a row does not see do not reach it.
+ *   - A row that sees nothing gives O = 0 and a log normaliser of -inf; so does one whose scores are all -inf
+ *     over finite values. Infinities and NaN in keys and values that a row does not see do not reach it.
  *   - Rows of O (and of the log normalisers) behind the last sequence are left as they are.
  *   - Nothing is allocated and nothing waits for the host: every call can be captured into a graph. Workspaces
  *     belong to the caller (16-byte aligned, contents undefined, free for reuse once the call has run);
