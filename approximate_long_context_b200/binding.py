@@ -34,7 +34,7 @@ EXPORTS = [
     "hyper_attn_diagnostics", "hyper_attn_backward", "hyper_attn_test_fail_alloc",
     "hyper_attn_prompt", "hyper_attn_prompt_workspace", "hyper_attn_tree", "hyper_attn_tree_workspace",
     "hyper_attn_cache_free", "hyper_attn_cache_fork", "hyper_attn_cache_workspace", "hyper_attn_cache_reserve",
-    "hyper_attn_cache_append", "hyper_attn_cache_commit",
+    "hyper_attn_cache_append", "hyper_attn_cache_commit", "hyper_attn_capturing",
 ]
 KERNEL_CLASSES = ["hash", "sort", "attn", "causal_base", "draws", "prompt", "tree", "cache"]
 
@@ -126,6 +126,7 @@ def lib():
     L.hyper_attn_prompt.argtypes = [vp, ctypes.POINTER(PromptArgs)]
     L.hyper_attn_prompt_workspace.argtypes = [vp, i64, i64, ci, ci]
     L.hyper_attn_prompt_workspace.restype = st
+    L.hyper_attn_capturing.argtypes = [vp]
     cache = ctypes.POINTER(CacheArgs)
     L.hyper_attn_tree.argtypes = [vp, cache, ctypes.POINTER(TreeArgs)]
     L.hyper_attn_tree_workspace.argtypes = [vp, ci]
@@ -258,6 +259,8 @@ class HyperAttention:
         self.options = default_options()
         self.device = device
         self._device_object = None
+        self._ws, self._ws_ptr, self._ws_bytes = None, 0, 0
+        self._captured = []
 
     def _check(self, rc: int):
         if rc:
@@ -277,6 +280,8 @@ class HyperAttention:
         o.test_stall_ms = test_stall_ms
         o.sampling = SAMPLING[sampling]
         self._check(lib().hyper_attn_set_options(self._h, ctypes.byref(o)))
+        if o.stream != self.options.stream:   # the buffer's reuse was ordered by the old stream
+            self._ws, self._ws_ptr, self._ws_bytes = None, 0, 0
         self.options = o
 
     def forward(self, Q, K, V, O, *, n, d, heads, block, m, r, causal, seed):
@@ -322,17 +327,27 @@ class HyperAttention:
             raise ValueError(f"{what}: on the handle's device")
         return t.data_ptr(), stride[0], stride[1]
 
-    def _workspace(self, nbytes: int):
-        """A device buffer whose reuse is ordered by the handle's stream (a graph under capture gets its own)."""
+    def _workspace(self, nbytes: int) -> int:
+        """The address of a device buffer of at least nbytes. Eager calls share one, in the order of the handle's stream; a
+        call under capture gets its own, from the graph's memory."""
         if not nbytes:
-            return None
+            return 0
+        capturing = _lib.hyper_attn_capturing(self._h)
+        if nbytes <= self._ws_bytes and not capturing:
+            return self._ws_ptr
         torch = _torch or _import_torch()
         stream = self.options.stream or 0
         if stream == torch.cuda.current_stream(self.device).cuda_stream:
-            return torch.empty(nbytes, dtype=torch.uint8, device=self._torch_device())
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self._torch_device()) if stream
-                               else torch.cuda.default_stream(self.device)):
-            return torch.empty(nbytes, dtype=torch.uint8, device=self._torch_device())
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=self._torch_device())
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self._torch_device()) if stream
+                                   else torch.cuda.default_stream(self.device)):
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=self._torch_device())
+        if not capturing:
+            self._ws, self._ws_ptr, self._ws_bytes = ws, ws.data_ptr(), nbytes
+        elif not torch.cuda.is_current_stream_capturing():
+            self._captured.append(ws)   # a capture that torch does not know of: its memory is not the graph's
+        return ws.data_ptr()
 
     def _torch_device(self):
         if self._device_object is None:
@@ -371,7 +386,7 @@ class HyperAttention:
         rc = L.prompt_packed(self._h, _PROMPT.pack(
             q[0], k[0], v[0], o[0], self._lse(lse, heads, tokens) or 0, tokens, q[1], q[2], k[1], k[2], v[1], v[2], o[1], o[2],
             heads, kv_heads, d, at, seqs, max(tokens, 1) if max_len is None else max_len, scale,
-            ws.data_ptr() if nbytes else 0, nbytes))
+            ws, nbytes))
         if rc:
             self._check(rc)
 
@@ -400,7 +415,7 @@ class HyperAttention:
             q[0], o[0], self._lse(lse, heads, tokens) or 0, tokens, q[1], q[2], o[1], o[2], heads, layer,
             0 if slots is None else _ints(slots, self.device, "slots", seqs), at,
             0 if mask is None else _ints(mask, self.device, "mask", tokens, True), seqs, max_draft, scale,
-            ws.data_ptr() if nbytes else 0, nbytes))
+            ws, nbytes))
         if rc:
             self._check(rc)
 
@@ -428,7 +443,7 @@ class HyperAttention:
         ws = self._workspace(nbytes)
         rc = L.hyper_attn_cache_reserve(
             self._h, c, _ints(slots, self.device, "slots"), _ints(add, self.device, "add", n), n,
-            None if granted is None else _ints(granted, self.device, "granted", n), ws.data_ptr(), nbytes)
+            None if granted is None else _ints(granted, self.device, "granted", n), ws, nbytes)
         if rc:
             self._check(rc)
 

@@ -23,6 +23,7 @@ __device__ __forceinline__ bool block_contains(const int32_t *list, int n, int32
 }
 
 __global__ void __launch_bounds__(256) cache_free_kernel(const ServeCache c, const int32_t *slots, int *status) {
+    grid_dependency_wait();
     const int i = blockIdx.x;
     const int32_t s = slots[i];
     const bool dup = block_contains(slots, i, s);
@@ -52,6 +53,7 @@ __global__ void __launch_bounds__(256) cache_free_kernel(const ServeCache c, con
 // Sources are read as they were before the call: a source that is also a destination of the call is refused.
 __global__ void __launch_bounds__(256) cache_fork_kernel(const ServeCache c, const int32_t *src, const int32_t *dst, int n,
                                                          int *status) {
+    grid_dependency_wait();
     const int i = blockIdx.x;
     const int32_t s = src[i], t = dst[i];
     bool bad = block_contains(dst, i, t);
@@ -132,12 +134,37 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *scratch, int64
     return x + (warp ? scratch[warp - 1] : 0);
 }
 
+// The committed rows (`rows` of each head) of page `from` go to page `to`, in one layer of k or v; THREADS threads take part.
+template <int THREADS>
+__device__ __forceinline__ void copy_page(const ServeCache &c, int esz, char *base, int64_t layer, int from, int to, int rows) {
+    const int64_t row_bytes = static_cast<int64_t>(c.d) * esz, head_bytes = row_bytes * c.page,
+                  page_bytes = head_bytes * c.kv_heads;
+    const char *src = base + (layer * c.pages + from) * page_bytes;
+    char *dst = base + (layer * c.pages + to) * page_bytes;
+    const int per_head = static_cast<int>(rows * row_bytes / 16);
+    const int total = per_head * c.kv_heads;
+    for (int x0 = threadIdx.x; x0 < total; x0 += THREADS * 4) {
+        int4 buf[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int x = x0 + THREADS * u;
+            if (x < total) buf[u] = *reinterpret_cast<const int4 *>(src + (x / per_head) * head_bytes + (x % per_head) * 16);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int x = x0 + THREADS * u;
+            if (x < total) *reinterpret_cast<int4 *>(dst + (x / per_head) * head_bytes + (x % per_head) * 16) = buf[u];
+        }
+    }
+}
+
 // One block plans the call: what each entry needs, the lowest free pages, and who gets which. One block because the
 // order matters (list order, lowest page first) and the data is small: the scan of the reference counts reads 16 of
 // them per thread and stops as soon as enough free pages are found.
 __global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const ServeCache c, const int32_t *slots,
                                                                           const int32_t *add, int n, int32_t *granted,
-                                                                          void *ws, int *status) {
+                                                                          void *ws, int esz, bool copy, int *status) {
+    grid_dependency_wait();
     __shared__ int64_t scratch[33];
     const ReservePlan p = reserve_plan(ws, n);
     const int tid = threadIdx.x;
@@ -259,35 +286,23 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const 
             row[p.held[i] + j] = id;
         }
     }
+    // 5. few copies are made here, without a second launch
+    if (copy) {
+        __syncthreads();
+        for (int i = 0; i < n; ++i)
+            if (p.from[i] >= 0 && p.to[i] >= 0)
+                for (int y = 0; y < 2 * static_cast<int>(c.layers); ++y)
+                    copy_page<kPlanThreads>(c, esz, static_cast<char *>((y & 1) ? c.v : c.k), y >> 1, p.from[i], p.to[i], p.rows[i]);
+    }
 }
 
-// The committed rows of a shared last page go to its copy: one block per (entry, layer, k or v).
+// One block per (entry, layer, k or v).
 __global__ void __launch_bounds__(256) cache_reserve_copy_kernel(const ServeCache c, int esz, int n, void *ws) {
     grid_dependency_wait();
     const ReservePlan p = reserve_plan(ws, n);
     const int from = p.from[blockIdx.x], to = p.to[blockIdx.x];
     if (from < 0 || to < 0) return;
-    const int64_t layer = blockIdx.y >> 1;
-    char *base = static_cast<char *>((blockIdx.y & 1) ? c.v : c.k);
-    const int64_t row_bytes = static_cast<int64_t>(c.d) * esz, head_bytes = row_bytes * c.page,
-                  page_bytes = head_bytes * c.kv_heads;
-    const char *src = base + (layer * c.pages + from) * page_bytes;
-    char *dst = base + (layer * c.pages + to) * page_bytes;
-    const int per_head = static_cast<int>(p.rows[blockIdx.x] * row_bytes / 16);
-    const int total = per_head * c.kv_heads;
-    for (int x0 = threadIdx.x; x0 < total; x0 += 256 * 4) {
-        int4 buf[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int x = x0 + 256 * u;
-            if (x < total) buf[u] = *reinterpret_cast<const int4 *>(src + (x / per_head) * head_bytes + (x % per_head) * 16);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int x = x0 + 256 * u;
-            if (x < total) *reinterpret_cast<int4 *>(dst + (x / per_head) * head_bytes + (x % per_head) * 16) = buf[u];
-        }
-    }
+    copy_page<256>(c, esz, static_cast<char *>((blockIdx.y & 1) ? c.v : c.k), blockIdx.y >> 1, from, to, p.rows[blockIdx.x]);
 }
 
 struct AppendArgs {
@@ -302,6 +317,7 @@ constexpr int kAppendLayers = 4;   // layers per block
 __global__ void __launch_bounds__(256) cache_append_kernel(const ServeCache c, int esz, const int32_t *slots,
                                                            const int32_t *cu, int n, int64_t tokens, const AppendArgs a,
                                                            int *status) {
+    grid_dependency_wait();
     const int64_t t = blockIdx.x;
     // the sequence that holds token t: the last one whose offset is not behind it
     int lo = 0, hi = n;
@@ -384,21 +400,14 @@ __device__ bool commit_entry(const ServeCache &c, const int32_t *slots, const in
 
 constexpr int kMoveChunk = 256;   // kept rows staged at a time
 
-// The kept rows of a draft move to the front of it: row len + keep[i] -> len + i, one block per (entry, layer, k or v).
-// keep is ascending, so keep[i] >= i and a row is read before a later row is written over it; every thread moves its
-// own 16-byte column in ascending order, eight rows in flight.
-__global__ void __launch_bounds__(128) cache_commit_move_kernel(const ServeCache c, int esz, const int32_t *slots,
-                                                                const int32_t *counts, const int32_t *keep,
-                                                                int64_t max_keep) {
-    __shared__ int64_t from[kMoveChunk], to[kMoveChunk];   // byte offsets of the rows in a layer, head 0
-    int len = 0, held = 0, count = 0;
-    if (!commit_entry(c, slots, counts, keep, max_keep, blockIdx.x, &len, &held, &count)) return;   // flagged below
-    const int32_t *mine = keep + static_cast<int64_t>(blockIdx.x) * max_keep;
-    const int32_t *row = c.table + static_cast<int64_t>(slots[blockIdx.x]) * c.max_pages;
+// The kept rows of a draft move to the front of it, in one layer of k or v: row len + keep[i] -> len + i. keep is ascending,
+// so keep[i] >= i and a row is read before a later row is written over it; every thread moves its own 16-byte column in
+// ascending order, eight rows in flight.
+__device__ __forceinline__ void move_rows(const ServeCache &c, int esz, char *base, int64_t layer, const int32_t *row, int len,
+                                          const int32_t *mine, int count, int64_t *from, int64_t *to) {
     const int64_t row_bytes = static_cast<int64_t>(c.d) * esz, head_bytes = row_bytes * c.page,
                   page_bytes = head_bytes * c.kv_heads;
-    const int64_t layer = blockIdx.y >> 1;
-    char *base = static_cast<char *>((blockIdx.y & 1) ? c.v : c.k) + layer * c.pages * page_bytes;
+    base += layer * c.pages * page_bytes;
     const int per_row = static_cast<int>(row_bytes / 16), total = per_row * c.kv_heads;
     for (int first = 0; first < count; first += kMoveChunk) {
         const int m = min(kMoveChunk, count - first);
@@ -424,10 +433,25 @@ __global__ void __launch_bounds__(128) cache_commit_move_kernel(const ServeCache
     }
 }
 
-// Lengths grow by the kept rows; the pages behind the new length are released.
-__global__ void __launch_bounds__(128) cache_commit_kernel(const ServeCache c, const int32_t *slots, const int32_t *counts,
-                                                           const int32_t *keep, int64_t max_keep, int *status) {
+// One block per (entry, layer, k or v).
+__global__ void __launch_bounds__(128) cache_commit_move_kernel(const ServeCache c, int esz, const int32_t *slots,
+                                                                const int32_t *counts, const int32_t *keep,
+                                                                int64_t max_keep) {
     grid_dependency_wait();
+    __shared__ int64_t from[kMoveChunk], to[kMoveChunk];   // byte offsets of the rows in a layer, head 0
+    int len = 0, held = 0, count = 0;
+    if (!commit_entry(c, slots, counts, keep, max_keep, blockIdx.x, &len, &held, &count)) return;   // flagged below
+    move_rows(c, esz, static_cast<char *>((blockIdx.y & 1) ? c.v : c.k), blockIdx.y >> 1,
+              c.table + static_cast<int64_t>(slots[blockIdx.x]) * c.max_pages, len,
+              keep + static_cast<int64_t>(blockIdx.x) * max_keep, count, from, to);
+}
+
+// Lengths grow by the kept rows; the pages behind the new length are released. move: the rows are moved here first.
+__global__ void __launch_bounds__(128) cache_commit_kernel(const ServeCache c, int esz, const int32_t *slots,
+                                                           const int32_t *counts, const int32_t *keep, int64_t max_keep,
+                                                           bool move, int *status) {
+    grid_dependency_wait();
+    __shared__ int64_t from[kMoveChunk], to[kMoveChunk];
     int len = 0, held = 0, count = 0;
     if (!commit_entry(c, slots, counts, keep, max_keep, blockIdx.x, &len, &held, &count)) {
         if (threadIdx.x == 0) atomicOr(status, kStatusData);
@@ -435,6 +459,12 @@ __global__ void __launch_bounds__(128) cache_commit_kernel(const ServeCache c, c
     }
     const int32_t s = slots[blockIdx.x];
     int32_t *row = c.table + static_cast<int64_t>(s) * c.max_pages;
+    if (move) {
+        for (int y = 0; y < 2 * static_cast<int>(c.layers); ++y)
+            move_rows(c, esz, static_cast<char *>((y & 1) ? c.v : c.k), y >> 1, row, len,
+                      keep + static_cast<int64_t>(blockIdx.x) * max_keep, count, from, to);
+        __syncthreads();   // the table has been read
+    }
     const int after = (len + count + c.page - 1) >> c.page_shift;
     for (int p = after + threadIdx.x; p < held; p += blockDim.x) {
         atomicSub(c.refs + row[p], 1);
@@ -452,20 +482,28 @@ size_t cache_workspace(int64_t n, int64_t pages) {
     return static_cast<size_t>(n) * (sizeof(int64_t) + 5 * sizeof(int32_t)) + static_cast<size_t>(pages) * sizeof(int32_t);
 }
 
+// All of these start behind the previous kernel of the stream without waiting for its last block to drain (they wait
+// themselves): a cache step is a chain of short kernels, and this takes about a microsecond off each.
+
 int launch_cache_free(const ServeCache &c, const int32_t *slots, int n, int *status, cudaStream_t st) {
-    cache_free_kernel<<<n, 256, 0, st>>>(c, slots, status);
-    return cudaPeekAtLastError() == cudaSuccess ? 1 : -1;
+    return launch_dependent(cache_free_kernel, dim3(n), dim3(256), 0, st, c, slots, status) ? 1 : -1;
 }
 
 int launch_cache_fork(const ServeCache &c, const int32_t *src, const int32_t *dst, int n, int *status, cudaStream_t st) {
-    cache_fork_kernel<<<n, 256, 0, st>>>(c, src, dst, n, status);
-    return cudaPeekAtLastError() == cudaSuccess ? 1 : -1;
+    return launch_dependent(cache_fork_kernel, dim3(n), dim3(256), 0, st, c, src, dst, n, status) ? 1 : -1;
 }
+
+// Bytes of one row in all layers of k and v.
+static int64_t row_bytes_all(const ServeCache &c, int esz) { return 2 * c.layers * c.kv_heads * c.d * esz; }
 
 int launch_cache_reserve(const ServeCache &c, int esz, const int32_t *slots, const int32_t *add, int n, int32_t *granted,
                          void *ws, int *status, cudaStream_t st) {
-    cache_reserve_plan_kernel<<<1, kPlanThreads, 0, st>>>(c, slots, add, n, granted, ws, status);
-    if (cudaPeekAtLastError() != cudaSuccess) return -1;
+    // up to about 256 KB the planning block copies as fast as a second launch starts
+    const bool copy = n * c.page * row_bytes_all(c, esz) <= 256 * 1024;
+    if (!launch_dependent(cache_reserve_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, c, slots, add, n, granted, ws, esz, copy,
+                          status))
+        return -1;
+    if (copy) return 1;
     const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(2 * c.layers));
     return launch_dependent(cache_reserve_copy_kernel, grid, dim3(256), 0, st, c, esz, n, ws) ? 2 : -1;
 }
@@ -481,20 +519,21 @@ int launch_cache_append(const ServeCache &c, int esz, const int32_t *slots, cons
     a.layer = layer;
     a.layers = layers;
     const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>((layers + kAppendLayers - 1) / kAppendLayers));
-    cache_append_kernel<<<grid, 256, 0, st>>>(c, esz, slots, cu, n, tokens, a, status);
-    return cudaPeekAtLastError() == cudaSuccess ? 1 : -1;
+    return launch_dependent(cache_append_kernel, grid, dim3(256), 0, st, c, esz, slots, cu, n, tokens, a, status) ? 1 : -1;
 }
 
 int launch_cache_commit(const ServeCache &c, int esz, const int32_t *slots, const int32_t *counts, const int32_t *keep,
                         int64_t max_keep, int n, int *status, cudaStream_t st) {
+    // small moves (a row of all layers within 16 KB) are made by the block that commits the entry
+    const bool move = keep && row_bytes_all(c, esz) <= 16 * 1024;
     int launches = 0;
-    if (keep) {
+    if (keep && !move) {
         const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(2 * c.layers));
-        cache_commit_move_kernel<<<grid, 128, 0, st>>>(c, esz, slots, counts, keep, max_keep);
-        if (cudaPeekAtLastError() != cudaSuccess) return -1;
+        if (!launch_dependent(cache_commit_move_kernel, grid, dim3(128), 0, st, c, esz, slots, counts, keep, max_keep)) return -1;
         ++launches;
     }
-    if (!launch_dependent(cache_commit_kernel, dim3(n), dim3(128), 0, st, c, slots, counts, keep, max_keep, status)) return -1;
+    if (!launch_dependent(cache_commit_kernel, dim3(n), dim3(128), 0, st, c, esz, slots, counts, keep, max_keep, move, status))
+        return -1;
     return launches + 1;
 }
 

@@ -123,6 +123,7 @@ struct TreeWalk {
     int seq;               // sequence of `at`
     int64_t seq_first;     // number of its first key tile
     TreeSeq x;
+    TreeSeq lane_seq;      // sequence `lane` where the call has at most 32: each is read once
     int nk, tiles;
 
     static __device__ __forceinline__ int tiles_of(const ServeArgs &a, const TreeSeq &x, int tile_rows, int tok_tile) {
@@ -144,6 +145,7 @@ struct TreeWalk {
             y.t = 0;
             if (b + lane < a.seqs) ok &= tree_seq(a, b + lane, &y);
             total += cost(a, y, key_tile, tile_rows, tok_tile);
+            lane_seq = y;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -158,9 +160,11 @@ struct TreeWalk {
         // the sequence that holds `first`
         int64_t run = 0;
         for (int b = 0; b < a.seqs; b += 32) {
-            TreeSeq y;
-            y.t = 0;
-            if (b + lane < a.seqs) tree_seq(a, b + lane, &y);
+            TreeSeq y = lane_seq;
+            if (a.seqs > 32) {
+                y.t = 0;
+                if (b + lane < a.seqs) tree_seq(a, b + lane, &y);
+            }
             const int64_t mine = cost(a, y, key_tile, tile_rows, tok_tile);
             int64_t sum = mine;
 #pragma unroll
@@ -180,7 +184,14 @@ struct TreeWalk {
         load(a, key_tile, tile_rows, tok_tile);
     }
     __device__ __forceinline__ void load(const ServeArgs &a, int key_tile, int tile_rows, int tok_tile) {
-        tree_seq(a, seq, &x);
+        if (a.seqs > 32) {
+            tree_seq(a, seq, &x);
+        } else {
+            x.start = __shfl_sync(0xffffffffu, lane_seq.start, seq);
+            x.t = __shfl_sync(0xffffffffu, lane_seq.t, seq);
+            x.len = __shfl_sync(0xffffffffu, lane_seq.len, seq);
+            x.table = __shfl_sync(0xffffffffu, lane_seq.table, seq);
+        }
         nk = x.t ? (x.len + x.t + key_tile - 1) / key_tile : 0;
         tiles = tiles_of(a, x, tile_rows, tok_tile);
     }

@@ -92,6 +92,15 @@ int launched(hyper_attn_t h, int k, const char *what) {
 
 extern "C" {
 
+int hyper_attn_capturing(hyper_attn_t h) {
+    cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+    if (!h || cudaStreamIsCapturing(static_cast<cudaStream_t>(h->opt.stream), &s) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return s != cudaStreamCaptureStatusNone;
+}
+
 size_t hyper_attn_prompt_workspace(hyper_attn_t h, int64_t tokens, int64_t seqs, int heads, int kv_heads) {
     if (!h || tokens < 0 || seqs < 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads) return 0;
     return ha::serve_prompt_workspace(tokens, seqs, kv_heads, heads / kv_heads, h->sms);

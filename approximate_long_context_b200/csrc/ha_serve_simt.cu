@@ -274,6 +274,7 @@ template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const ServeArgs a) {
     extern __shared__ __align__(16) float sm[];
     __shared__ Work shared;
+    grid_dependency_wait();
     const int kh = static_cast<int>(blockIdx.x % a.kv_heads);
     const int64_t want = blockIdx.x / a.kv_heads;
     if (threadIdx.x < 32) {
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const ServeArgs a) 
     extern __shared__ __align__(16) float sm[];
     __shared__ TreePiece piece;
     __shared__ int more;
+    grid_dependency_wait();
     TreeWalk walk;
     const int warp = threadIdx.x >> 5, blocks = gridDim.x, block = blockIdx.x;
     if (warp == 0) walk.begin(a, kBN, kBM, 0, block, blocks);
@@ -448,8 +450,8 @@ int prompt_simt(const ServeArgs &a, cudaStream_t st) {
     if (!allow_smem(prompt_simt_kernel<D, T>, Smem<D>::kBytes, &known)) return -1;
     if ((a.tokens * a.group / kBM + a.seqs) * a.kv_heads > 0x7fffffff) return -2;   // blocks of a grid
     const int64_t tiles = a.tokens * a.group / kBM + a.seqs;   // at most: one ragged tile per sequence
-    prompt_simt_kernel<D, T><<<static_cast<unsigned>(tiles * a.kv_heads), kThreads, Smem<D>::kBytes, st>>>(a);
-    return cudaPeekAtLastError() == cudaSuccess ? 1 : -1;
+    const dim3 grid(static_cast<unsigned>(tiles * a.kv_heads));
+    return launch_dependent(prompt_simt_kernel<D, T>, grid, dim3(kThreads), Smem<D>::kBytes, st, a) ? 1 : -1;
 }
 
 template <int D, typename T>
@@ -457,8 +459,7 @@ int tree_simt(const ServeArgs &a, cudaStream_t st) {
     static std::atomic<uint64_t> known{0};
     if (!allow_smem(tree_simt_kernel<D, T>, Smem<D>::kBytes, &known)) return -1;
     const int blocks = 2 * a.sms;   // two per SM fit (shared memory)
-    tree_simt_kernel<D, T><<<blocks, kThreads, Smem<D>::kBytes, st>>>(a);
-    if (cudaPeekAtLastError() != cudaSuccess) return -1;
+    if (!launch_dependent(tree_simt_kernel<D, T>, dim3(blocks), dim3(kThreads), Smem<D>::kBytes, st, a)) return -1;
     return launch_tree_join(a, blocks, kBM, st) ? 2 : -1;
 }
 

@@ -155,6 +155,7 @@ struct PromptPlan {
 };
 
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const ServeArgs a, int pair_tokens, int capacity) {
+    grid_dependency_wait();
     __shared__ int cursor[kPlanBuckets];
     __shared__ int singles;
     __shared__ int sums[32];
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + C::kTmemSlot);
-    grid_dependency_wait();   // the list of prompt items, if a kernel in front of this one makes it
+    grid_dependency_wait();   // what was in front on the stream, the list of prompt items among it
 
     // a wait of a whole warp: all of its lanes go on or none
     auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, bar_wait(b, parity, abort_flag)); };
@@ -1129,13 +1130,11 @@ bool make_rows_map(CUtensorMap *map, const void *base, int d, int heads, int64_t
 }
 
 template <int D, int MODE>
-bool launch(const TcArgs &x, const Maps &maps, int blocks, bool dependent, cudaStream_t st) {
+bool launch(const TcArgs &x, const Maps &maps, int blocks, cudaStream_t st) {
     using C = Cfg<D, MODE>;
     static std::atomic<uint64_t> known{0};
     if (!allow_smem(serve_tc_kernel<D, MODE>, C::kBytes, &known)) return false;
-    if (dependent) return launch_dependent(serve_tc_kernel<D, MODE>, dim3(blocks), dim3(kThreads), C::kBytes, st, x, maps);
-    serve_tc_kernel<D, MODE><<<blocks, kThreads, C::kBytes, st>>>(x, maps);
-    return cudaPeekAtLastError() == cudaSuccess;
+    return launch_dependent(serve_tc_kernel<D, MODE>, dim3(blocks), dim3(kThreads), C::kBytes, st, x, maps);
 }
 
 // Items of a prompt call: every sequence has at most one pair of tiles that is not full.
@@ -1169,12 +1168,12 @@ int launch_prompt_tc(const ServeArgs &a, cudaStream_t st) {
         !make_rows_map(&maps.v, a.v, a.d, a.kv_heads, a.tokens, a.v_head, a.v_tok, 1, 128))
         return -2;
     if (x.plan) {
-        prompt_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, 2 * x.tpt, static_cast<int>(items));
-        if (cudaPeekAtLastError() != cudaSuccess) return -1;
+        if (!launch_dependent(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, 2 * x.tpt, static_cast<int>(items)))
+            return -1;
     }
     const int64_t most = items * a.kv_heads;
     const int blocks = static_cast<int>(most < a.sms ? most : a.sms);
-    const bool ok = a.d == 64 ? launch<64, PROMPT>(x, maps, blocks, x.plan, st) : launch<128, PROMPT>(x, maps, blocks, x.plan, st);
+    const bool ok = a.d == 64 ? launch<64, PROMPT>(x, maps, blocks, st) : launch<128, PROMPT>(x, maps, blocks, st);
     return ok ? 1 + x.plan : -1;
 }
 
@@ -1194,8 +1193,8 @@ int launch_tree_tc(const ServeArgs &a, cudaStream_t st) {
         !make_map(&maps.k, a.kp, 4, dims, strides, box) || !make_map(&maps.v, a.vp, 4, dims, strides, box))
         return -2;
     bool ok;
-    if (alt) ok = a.d == 64 ? launch<64, TREE_ALT>(x, maps, a.sms, false, st) : launch<128, TREE_ALT>(x, maps, a.sms, false, st);
-    else ok = a.d == 64 ? launch<64, TREE_PAIR>(x, maps, a.sms, false, st) : launch<128, TREE_PAIR>(x, maps, a.sms, false, st);
+    if (alt) ok = a.d == 64 ? launch<64, TREE_ALT>(x, maps, a.sms, st) : launch<128, TREE_ALT>(x, maps, a.sms, st);
+    else ok = a.d == 64 ? launch<64, TREE_PAIR>(x, maps, a.sms, st) : launch<128, TREE_PAIR>(x, maps, a.sms, st);
     if (!ok) return -1;
     return launch_tree_join(a, a.sms, alt ? 128 : 256, st) ? 2 : -1;
 }

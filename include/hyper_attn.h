@@ -315,6 +315,10 @@ HA_API int hyper_attn_forward_noalloc(const void *Q, const void *K, const void *
  *   - Equal calls give equal bits.
  */
 
+/* 1 while the handle's stream is being captured into a graph, 0 otherwise. (A caller that keeps one workspace for
+ * its eager calls has to give a captured call one of its own.) */
+HA_API int hyper_attn_capturing(hyper_attn_t h);
+
 /* Causal attention over packed prompts: row i of a sequence sees rows 0..i of the same sequence. */
 typedef struct {
     const void *q, *k, *v;
