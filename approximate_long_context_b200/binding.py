@@ -124,7 +124,7 @@ def lib():
     L.hyper_attn_profile_read.argtypes = [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ci), ci]
     st = ctypes.c_size_t
     L.hyper_attn_prompt.argtypes = [vp, ctypes.POINTER(PromptArgs)]
-    L.hyper_attn_prompt_workspace.argtypes = [vp, i64, i64, ci, ci]
+    L.hyper_attn_prompt_workspace.argtypes = [vp, i64, i64, i64, ci, ci]
     L.hyper_attn_prompt_workspace.restype = st
     L.hyper_attn_capturing.argtypes = [vp]
     cache = ctypes.POINTER(CacheArgs)
@@ -381,11 +381,13 @@ class HyperAttention:
         at = _ints(offsets, self.device, "offsets")
         seqs = offsets.numel() - 1
         L = _lib
-        nbytes = L.hyper_attn_prompt_workspace(self._h, tokens, seqs, heads, kv_heads)
+        if max_len is None:
+            max_len = max(tokens, 1)
+        nbytes = L.hyper_attn_prompt_workspace(self._h, tokens, seqs, max_len, heads, kv_heads)
         ws = self._workspace(nbytes)
         rc = L.prompt_packed(self._h, _PROMPT.pack(
             q[0], k[0], v[0], o[0], self._lse(lse, heads, tokens) or 0, tokens, q[1], q[2], k[1], k[2], v[1], v[2], o[1], o[2],
-            heads, kv_heads, d, at, seqs, max(tokens, 1) if max_len is None else max_len, scale,
+            heads, kv_heads, d, at, seqs, max_len, scale,
             ws, nbytes))
         if rc:
             self._check(rc)

@@ -166,62 +166,71 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const 
                                                                           void *ws, int esz, bool copy, int *status) {
     grid_dependency_wait();
     __shared__ int64_t scratch[33];
+    __shared__ int32_t slot_of[kPlanThreads], last_of[kPlanThreads];   // of 1024 entries at a time
     const ReservePlan p = reserve_plan(ws, n);
     const int tid = threadIdx.x;
-    // 1. what each entry would append to; an entry out of range, or a slot's second one, asks for nothing
-    for (int i = tid; i < n; i += kPlanThreads) {
-        const int32_t s = slots[i];
-        int last = -1, held = -1;
-        bool ok = s >= 0 && s < c.slots && add[i] >= 0;
-        for (int j = 0; ok && j < i; ++j) ok = slots[j] != s;
-        if (ok) {
-            const int64_t len = c.lens[s];
-            held = c.held[s];
-            const int64_t pages = (len + add[i] + c.page - 1) >> c.page_shift;
-            ok = len >= 0 && held >= 0 && held <= c.max_pages && ((len + c.page - 1) >> c.page_shift) <= held &&
-                 pages <= c.max_pages;
-            if (ok && (len & (c.page - 1)) != 0 && add[i] > 0) {
-                last = c.table[s * c.max_pages + (len >> c.page_shift)];
-                ok = last >= 0 && last < c.pages;
-            }
-        }
-        if (!ok) {
-            atomicOr(status, kStatusData);
-            last = held = -1;
-        }
-        p.last[i] = last;
-        p.held[i] = held;
+    // the first reference counts, on their way while the entries are looked over
+    const bool ahead = tid * 16 + 16 <= c.pages;
+    int4 first_refs[4];
+    if (ahead) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) first_refs[q] = *reinterpret_cast<const int4 *>(c.refs + tid * 16 + 4 * q);
     }
-    __syncthreads();
-    // 2. pages needed, in list order: a shared last page is copied by every entry but the last one that holds it
+    // 1. what each entry would append to (an entry out of range, or a slot's second one, asks for nothing), and
+    // 2. the pages it needs, in list order: a shared last page is copied by every entry but the last one that holds it
     int64_t carry = 0;
     for (int base = 0; base < n; base += kPlanThreads) {
         const int i = base + tid;
+        const int32_t s = i < n ? slots[i] : -1;
+        const int32_t want = i < n ? add[i] : 0;
+        __syncthreads();   // the 1024 entries before have been read
+        slot_of[tid] = s;
+        __syncthreads();
+        bool ok = i < n && s >= 0 && s < c.slots && want >= 0;
+        int64_t len = 0, pages = 0;
+        int held = -1, last = -1, shared = 0;
+        if (ok) {
+            len = c.lens[s];
+            held = c.held[s];
+            pages = (len + want + c.page - 1) >> c.page_shift;
+            ok = len >= 0 && held >= 0 && held <= c.max_pages && ((len + c.page - 1) >> c.page_shift) <= held &&
+                 pages <= c.max_pages;
+            if (ok && (len & (c.page - 1)) != 0 && want > 0) {
+                last = c.table[s * c.max_pages + (len >> c.page_shift)];
+                ok = last >= 0 && last < c.pages;
+                if (ok) shared = c.refs[last];
+            }
+        }
+        for (int j = 0; ok && j < tid; ++j) ok = slot_of[j] != s;
+        for (int j = 0; ok && j < base; ++j) ok = slots[j] != s;
+        if (!ok) {
+            last = held = -1;
+            if (i < n) atomicOr(status, kStatusData);
+        }
+        last_of[tid] = last;
+        if (i < n) {
+            p.last[i] = last;
+            p.held[i] = held;
+        }
+        __syncthreads();
         int64_t need = 0;
-        if (i < n && p.held[i] >= 0) {
-            const int64_t len = c.lens[slots[i]];
-            const int64_t pages = (len + add[i] + c.page - 1) >> c.page_shift;
-            need = pages > p.held[i] ? pages - p.held[i] : 0;
-            int from = -1;
-            if (p.last[i] >= 0) {
-                const int32_t last = p.last[i];
-                int shared = c.refs[last];
-                if (shared > 1)
-                    for (int j = 0; j < i; ++j) shared -= p.last[j] == last;
+        int from = -1;
+        if (ok) {
+            need = pages > held ? pages - held : 0;
+            if (last >= 0 && shared > 1) {
+                for (int j = 0; j < tid; ++j) shared -= last_of[j] == last;
+                for (int j = 0; j < base; ++j) shared -= p.last[j] == last;
                 if (shared > 1) from = last;
             }
-            p.from[i] = from;
-            p.rows[i] = static_cast<int32_t>(len & (c.page - 1));
             need += from >= 0;
-        } else if (i < n) {
-            p.from[i] = -1;
-            p.rows[i] = 0;
         }
         int64_t total;
         const int64_t sum = block_scan(need, scratch, &total);
         if (i < n) {
-            p.upto[i] = carry + sum;
+            p.from[i] = from;
             p.to[i] = -1;
+            p.rows[i] = static_cast<int32_t>(len & (c.page - 1));
+            p.upto[i] = carry + sum;
         }
         carry += total;
     }
@@ -234,7 +243,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const 
         if (first + 16 <= c.pages) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int4 r = *reinterpret_cast<const int4 *>(c.refs + first + 4 * q);
+                const int4 r = base == 0 ? first_refs[q] : *reinterpret_cast<const int4 *>(c.refs + first + 4 * q);
                 free |= static_cast<unsigned>((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << (4 * q);
             }
         } else {

@@ -156,7 +156,7 @@ struct ServeArgs {
     int sms;
 };
 
-size_t serve_prompt_workspace(int64_t tokens, int64_t seqs, int kv_heads, int group, int sms);
+size_t serve_prompt_workspace(int64_t tokens, int64_t seqs, int64_t max_len, int kv_heads, int group, int sms);
 size_t serve_tree_workspace(int sms, int d);
 // Return the number of kernels launched, -1 on a launch error.
 int launch_prompt_simt(const ServeArgs &a, int dtype, cudaStream_t st);

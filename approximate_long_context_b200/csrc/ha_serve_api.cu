@@ -101,9 +101,9 @@ int hyper_attn_capturing(hyper_attn_t h) {
     return s != cudaStreamCaptureStatusNone;
 }
 
-size_t hyper_attn_prompt_workspace(hyper_attn_t h, int64_t tokens, int64_t seqs, int heads, int kv_heads) {
+size_t hyper_attn_prompt_workspace(hyper_attn_t h, int64_t tokens, int64_t seqs, int64_t max_len, int heads, int kv_heads) {
     if (!h || tokens < 0 || seqs < 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads) return 0;
-    return ha::serve_prompt_workspace(tokens, seqs, kv_heads, heads / kv_heads, h->sms);
+    return ha::serve_prompt_workspace(tokens, seqs, max_len, kv_heads, heads / kv_heads, h->sms);
 }
 
 int hyper_attn_prompt(hyper_attn_t h, const ha_prompt_args *p) {
@@ -133,7 +133,7 @@ int hyper_attn_prompt(hyper_attn_t h, const ha_prompt_args *p) {
         if ((rc = check_strides(h, "v", p->tokens, p->kv_heads, p->d, ei, &a.v_tok, &a.v_head, false))) return rc;
         if ((rc = check_strides(h, "o", p->tokens, p->heads, p->d, eo, &a.o_tok, &a.o_head, true))) return rc;
         if (p->o == p->q || p->o == p->k || p->o == p->v) return fail(h, HA_ERR_INVALID_ARG, "O must not alias Q, K or V");
-        const size_t need = ha::serve_prompt_workspace(p->tokens, p->seqs, p->kv_heads, p->heads / p->kv_heads, h->sms);
+        const size_t need = ha::serve_prompt_workspace(p->tokens, p->seqs, p->max_len, p->kv_heads, p->heads / p->kv_heads, h->sms);
         if (need && (!p->workspace || !aligned16(p->workspace) || p->workspace_bytes < need))
             return fail(h, HA_ERR_INVALID_ARG, "workspace of %zu bytes needed, 16-byte aligned", need);
         a.tokens = p->tokens;

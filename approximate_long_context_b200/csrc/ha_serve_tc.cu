@@ -105,7 +105,7 @@ struct TcArgs {
     ServeArgs a;
     int tpt;         // query tokens of a tile
     int box_rows;    // rows that a Q load brings
-    int plan;        // prompt: items come from the list in the workspace
+    int order;       // prompt: where the items come from (PromptOrder)
 };
 
 // Wait for a phase of a barrier, at most about 2 s of global time. Inlined in few instructions: under a register split no
@@ -141,9 +141,12 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
 
 // ---------------------------------------------------------------------------------------------- prompt items
 //
-// The items of a prompt call (sequence, pair of query tiles) cost as many key tiles as lie in front of them. With many
-// sequences a one-block kernel lists them by falling position, so that the persistent blocks, which take them in turn
-// (to and fro), end together; with one sequence the list is known.
+// The items of a prompt call (sequence, pair of query tiles) cost as many key tiles as lie in front of them. In general a
+// one-block kernel lists them by falling position, so that the persistent blocks, which take them in turn (to and fro),
+// end together. No list is needed for one sequence, for fewer items than blocks (SCAN: the walk finds them in the
+// offsets), nor where no sequence is longer than a pair of tiles: all items cost alike then (PAIRS), and sequences of one
+// tile take two key heads at a time (SINGLES).
+enum PromptOrder { SCAN = 0, LIST = 1, PAIRS = 2, SINGLES = 3 };
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 4096;
@@ -157,7 +160,6 @@ struct PromptPlan {
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const ServeArgs a, int pair_tokens, int capacity) {
     grid_dependency_wait();
     __shared__ int cursor[kPlanBuckets];
-    __shared__ int singles;
     __shared__ int sums[32];
     PromptPlan *head = static_cast<PromptPlan *>(a.ws);
     int2 *list = reinterpret_cast<int2 *>(head + 1);
@@ -166,19 +168,41 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const ServeAr
     int shift = 0;
     while (((levels - 1) >> shift) + 2 > kPlanBuckets) ++shift;
     const int buckets = ((levels - 1) >> shift) + 2;   // the last one: sequences of one query tile
-    auto bucket = [&](int p, int len) { return 2 * len <= pair_tokens ? buckets - 1 : buckets - 2 - (p >> shift); };
+    // A lane reads a sequence; its pairs are handled by the lane itself, or by the whole warp if there are many. one(b, k)
+    // is called for k neighbouring entries of bucket b that belong to different lanes, many for one entry of a lane.
+    auto visit = [&](auto entry, bool report) {
+        bool ok = true;
+        for (int b = warp * 32; b < a.seqs; b += kPlanThreads) {
+            int start = 0, len = 0;
+            if (b + lane < a.seqs) ok &= prompt_seq(a, b + lane, &start, &len);
+            const int pairs = (len + pair_tokens - 1) / pair_tokens;
+            const bool single = len > 0 && 2 * len <= pair_tokens;
+            entry(single, buckets - 1, b + lane, 0);
+            const unsigned big = __ballot_sync(0xffffffffu, pairs > 4);
+            for (int p = 0; p < 4; ++p) {
+                const bool mine = !single && p < pairs && !(big >> lane & 1u);
+                if (__any_sync(0xffffffffu, mine)) entry(mine, buckets - 2 - (p >> shift), b + lane, p);
+            }
+            for (unsigned rest = big; rest; rest &= rest - 1) {
+                const int l = __ffs(rest) - 1, n = __shfl_sync(0xffffffffu, pairs, l);
+                for (int p0 = 0; p0 < n; p0 += 32) entry(p0 + lane < n, buckets - 2 - ((p0 + lane) >> shift), b + l, p0 + lane);
+            }
+        }
+        if (report && !ok) atomicOr(a.status, kStatusData);
+    };
+    // the place of an entry in its bucket; the lanes of a warp that meet in one bucket take their places with one addition
+    auto place = [&](bool mine, int b) -> int {
+        const unsigned same = __match_any_sync(0xffffffffu, mine ? b : -1);
+        const int leader = __ffs(same) - 1;
+        int at = 0;
+        if (mine && lane == leader) at = atomicAdd(&cursor[b], __popc(same));
+        return __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1u));
+    };
     for (int b = tid; b < buckets; b += kPlanThreads) cursor[b] = 0;
     __syncthreads();
-    bool ok = true;
-    for (int s = warp; s < a.seqs; s += 32) {
-        int start, len;
-        ok &= prompt_seq(a, s, &start, &len);
-        const int pairs = (len + pair_tokens - 1) / pair_tokens;
-        for (int p = lane; p < pairs; p += 32) atomicAdd(&cursor[bucket(p, len)], 1);
-    }
-    if (!ok && lane == 0) atomicOr(a.status, kStatusData);
+    visit([&](bool mine, int b, int, int) { place(mine, b); }, true);
     __syncthreads();
-    if (tid == 0) singles = cursor[buckets - 1];
+    const int singles = cursor[buckets - 1];
     // exclusive sums over the buckets, highest position first: four buckets per thread
     int mine[kPlanBuckets / kPlanThreads], sum = 0;
 #pragma unroll
@@ -216,15 +240,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const ServeAr
         head->single = max(0, singles - (sums[31] - head->count));
     }
     __syncthreads();
-    for (int s = warp; s < a.seqs; s += 32) {
-        int start, len;
-        prompt_seq(a, s, &start, &len);
-        const int pairs = (len + pair_tokens - 1) / pair_tokens;
-        for (int p = lane; p < pairs; p += 32) {
-            const int at = atomicAdd(&cursor[bucket(p, len)], 1);
-            if (at < capacity) list[at] = make_int2(s, p);
-        }
-    }
+    visit([&](bool mine, int b, int s, int p) {
+        const int at = place(mine, b);
+        if (mine && at < capacity) list[at] = make_int2(s, p);
+    }, false);
 }
 
 // The walk of one block over a prompt call's items, run by one whole warp.
@@ -237,7 +256,19 @@ struct PromptWalk {
         const ServeArgs &a = x.a;
         const int lane = threadIdx.x & 31;
         round = 0;
-        if (x.plan) {
+        if (x.order >= PAIRS) {
+            // the offsets are looked over here, as no list is made
+            bool ok = true;
+            if (blockIdx.x == 0)
+                for (int b = lane; b < a.seqs; b += 32) {
+                    int start, len;
+                    ok &= prompt_seq(a, b, &start, &len);
+                }
+            if (!ok) atomicOr(a.status, kStatusData);
+            count = static_cast<int64_t>(a.seqs) * (x.order == SINGLES ? (a.kv_heads + 1) >> 1 : a.kv_heads);
+            return;
+        }
+        if (x.order == LIST) {
             const PromptPlan *p = static_cast<const PromptPlan *>(a.ws);
             normal = static_cast<int64_t>(p->count - p->single) * a.kv_heads;
             count = normal + static_cast<int64_t>(p->single) * ((a.kv_heads + 1) >> 1);
@@ -258,11 +289,27 @@ struct PromptWalk {
     __device__ __forceinline__ bool next(const TcArgs &x, int *seq, int *pair, int *kh, bool *single) {
         const ServeArgs &a = x.a;
         const int lane = threadIdx.x & 31;
+        if (x.order >= PAIRS) {
+            const int half = (a.kv_heads + 1) >> 1;
+            for (;; ++round) {   // empty sequences are passed over
+                const int64_t i = round * gridDim.x + blockIdx.x;
+                if (i >= count) return false;
+                *single = x.order == SINGLES;
+                *seq = static_cast<int>(*single ? i / half : i / a.kv_heads);
+                *kh = *single ? 2 * static_cast<int>(i % half) : static_cast<int>(i % a.kv_heads);
+                *pair = 0;
+                int start, len;
+                prompt_seq(a, *seq, &start, &len);
+                if (len > 0) break;
+            }
+            ++round;
+            return true;
+        }
         const int64_t turn = (round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
         const int64_t i = round * gridDim.x + turn;
         ++round;
         if (i >= count) return false;   // the last round is not full
-        if (x.plan) {
+        if (x.order == LIST) {
             const int half = (a.kv_heads + 1) >> 1;
             *single = i >= normal;
             const int64_t at = *single ? normal / a.kv_heads + (i - normal) / half : i / a.kv_heads;
@@ -1140,16 +1187,17 @@ bool launch(const TcArgs &x, const Maps &maps, int blocks, cudaStream_t st) {
 // Items of a prompt call: every sequence has at most one pair of tiles that is not full.
 int64_t prompt_items(int64_t tokens, int64_t seqs, int tpt) { return tokens / (2 * tpt) + seqs; }
 
-// Whether the items are listed by a kernel of their own: not for one sequence, whose items are known, nor for fewer
-// items than blocks, which need no order (the extra launch takes about 3 us).
-bool prompt_plan(int64_t tokens, int64_t seqs, int kv_heads, int group, int sms) {
-    return seqs > 1 && prompt_items(tokens, seqs, 128 / group) * kv_heads > sms;
+// The list costs an extra launch (about 5 us) and is made only where the order of the items matters.
+int prompt_order(int64_t tokens, int64_t seqs, int64_t max_len, int kv_heads, int group, int sms) {
+    const int tpt = 128 / group;
+    if (seqs <= 1 || prompt_items(tokens, seqs, tpt) * kv_heads <= sms) return SCAN;
+    return max_len <= tpt ? SINGLES : max_len <= 2 * tpt ? PAIRS : LIST;
 }
 
 }  // namespace
 
-size_t serve_prompt_workspace(int64_t tokens, int64_t seqs, int kv_heads, int group, int sms) {
-    if (group > 128 || !prompt_plan(tokens, seqs, kv_heads, group, sms)) return 0;
+size_t serve_prompt_workspace(int64_t tokens, int64_t seqs, int64_t max_len, int kv_heads, int group, int sms) {
+    if (group > 128 || prompt_order(tokens, seqs, max_len, kv_heads, group, sms) != LIST) return 0;
     return sizeof(PromptPlan) + static_cast<size_t>(prompt_items(tokens, seqs, 128 / group)) * sizeof(int2);
 }
 
@@ -1161,20 +1209,20 @@ int launch_prompt_tc(const ServeArgs &a, cudaStream_t st) {
     x.box_rows = box_tokens * a.group;
     const int64_t items = prompt_items(a.tokens, a.seqs, x.tpt);
     if (items > 0x7fffffff) return -2;
-    x.plan = prompt_plan(a.tokens, a.seqs, a.kv_heads, a.group, a.sms);
+    x.order = prompt_order(a.tokens, a.seqs, a.max_len, a.kv_heads, a.group, a.sms);
     Maps maps;
     if (!make_rows_map(&maps.q, a.q, a.d, a.heads, a.tokens, a.q_head, a.q_tok, a.group, box_tokens) ||
         !make_rows_map(&maps.k, a.k, a.d, a.kv_heads, a.tokens, a.k_head, a.k_tok, 1, 128) ||
         !make_rows_map(&maps.v, a.v, a.d, a.kv_heads, a.tokens, a.v_head, a.v_tok, 1, 128))
         return -2;
-    if (x.plan) {
+    if (x.order == LIST) {
         if (!launch_dependent(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, 2 * x.tpt, static_cast<int>(items)))
             return -1;
     }
     const int64_t most = items * a.kv_heads;
     const int blocks = static_cast<int>(most < a.sms ? most : a.sms);
     const bool ok = a.d == 64 ? launch<64, PROMPT>(x, maps, blocks, st) : launch<128, PROMPT>(x, maps, blocks, st);
-    return ok ? 1 + x.plan : -1;
+    return ok ? 1 + (x.order == LIST) : -1;
 }
 
 int launch_tree_tc(const ServeArgs &a, cudaStream_t st) {

@@ -334,7 +334,8 @@ typedef struct {
     void *workspace;                  /* hyper_attn_prompt_workspace bytes; 0 bytes: may be NULL */
     size_t workspace_bytes;
 } ha_prompt_args;
-HA_API size_t hyper_attn_prompt_workspace(hyper_attn_t h, int64_t tokens, int64_t seqs, int heads, int kv_heads);
+HA_API size_t hyper_attn_prompt_workspace(hyper_attn_t h, int64_t tokens, int64_t seqs, int64_t max_len, int heads,
+                                          int kv_heads);
 HA_API int hyper_attn_prompt(hyper_attn_t h, const ha_prompt_args *args);
 
 /* A paged key/value cache in the caller's device memory. Slot s holds one sequence: its committed rows

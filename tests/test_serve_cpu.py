@@ -55,7 +55,7 @@ def test_null_handles_and_workspaces(lib):
     assert lib.hyper_attn_cache_append(None, binding.CacheArgs(), None, None, 0, 0, None, None, None, None, 0, 1) == inv
     assert lib.hyper_attn_cache_commit(None, binding.CacheArgs(), None, None, None, 0, 0) == inv
     assert lib.hyper_attn_tree_workspace(None, 64) == 0 and lib.hyper_attn_capturing(None) == 0
-    assert lib.hyper_attn_prompt_workspace(None, 1, 1, 1, 1) == 0
+    assert lib.hyper_attn_prompt_workspace(None, 1, 1, 1, 1, 1) == 0
     assert lib.hyper_attn_cache_workspace(-1, 5) == 0
     assert lib.hyper_attn_cache_workspace(7, 5) >= 7 * 8
 
