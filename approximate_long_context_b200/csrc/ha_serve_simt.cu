@@ -71,6 +71,7 @@ __device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float 
     float *Qs = sm + S::kQ, *Ks = sm + S::kK, *Ps = Ks, *Vs = sm + S::kV;
     const float c = a.scale * kLog2e;
     const T *q = static_cast<const T *>(a.q);
+    const bool busy = (tid >> 5) * 16 < w.rows;   // some row of the warp
     __syncthreads();   // the previous piece's reads are done
     for (int x = tid; x < kBM * (D / 4); x += kThreads) {
         const int r = x / (D / 4), col = (x % (D / 4)) * 4;
@@ -103,38 +104,47 @@ __device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float 
         const int base = kt * kBN;
         __syncthreads();   // the previous tile's P and V have been read
         bool odd = false;
-        for (int x = tid; x < kBN * (D / 4); x += kThreads) {
-            const int r = x / (D / 4), col = (x % (D / 4)) * 4;
-            float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-            if (base + r < keys) {
-                int64_t ko, vo;
-                const T *kp, *vp;
-                bool ok = true;
-                if (TREE) {
-                    const int key = base + r;
-                    const int32_t page = a.table[w.table + (key >> a.page_shift)];
-                    ok = page >= 0 && page < a.pages;
-                    if (!ok) atomicOr(a.status, kStatusData);
-                    const int64_t at = ((static_cast<int64_t>(page) * a.kv_heads + w.kh) << a.page_shift) +
-                                       (key & ((1 << a.page_shift) - 1));
-                    ko = vo = at * D + col;
-                    kp = static_cast<const T *>(a.kp);
-                    vp = static_cast<const T *>(a.vp);
-                } else {
-                    const int64_t row = w.start + base + r;
-                    ko = row * a.k_tok + w.kh * a.k_head + col;
-                    vo = row * a.v_tok + w.kh * a.v_head + col;
-                    kp = static_cast<const T *>(a.k);
-                    vp = static_cast<const T *>(a.v);
-                }
-                if (ok) {
-                    kv = load4<T>(kp + ko);
-                    vv = load4<T>(vp + vo);
+        // four rows' pieces of K and V in flight per thread (one after the other, a tile took eight memory latencies)
+        constexpr int kPer = kThreads / (D / 4), kBatch = 4;   // rows per turn of the block
+        const int col = (tid % (D / 4)) * 4;
+        for (int r0 = tid / (D / 4); r0 < kBN; r0 += kPer * kBatch) {
+            float4 kv[kBatch], vv[kBatch];
+            int64_t ko[kBatch], vo[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int key = base + r0 + u * kPer;
+                ko[u] = vo[u] = -1;
+                if (key < keys) {
+                    if (TREE) {
+                        const int32_t page = a.table[w.table + (key >> a.page_shift)];
+                        if (page >= 0 && page < a.pages) {
+                            ko[u] = vo[u] = (((static_cast<int64_t>(page) * a.kv_heads + w.kh) << a.page_shift) +
+                                             (key & ((1 << a.page_shift) - 1))) * D + col;
+                        } else {
+                            atomicOr(a.status, kStatusData);
+                        }
+                    } else {
+                        const int64_t row = w.start + key;
+                        ko[u] = row * a.k_tok + w.kh * a.k_head + col;
+                        vo[u] = row * a.v_tok + w.kh * a.v_head + col;
+                    }
                 }
             }
-            odd |= !finite4(vv);
-            *reinterpret_cast<float4 *>(Ks + r * S::LD + col) = kv;
-            *reinterpret_cast<float4 *>(Vs + r * S::LD + col) = vv;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                kv[u] = vv[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (ko[u] >= 0) {
+                    kv[u] = load4<T>(static_cast<const T *>(TREE ? a.kp : a.k) + ko[u]);
+                    vv[u] = load4<T>(static_cast<const T *>(TREE ? a.vp : a.v) + vo[u]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int r = r0 + u * kPer;
+                odd |= !finite4(vv[u]);
+                *reinterpret_cast<float4 *>(Ks + r * S::LD + col) = kv[u];
+                *reinterpret_cast<float4 *>(Vs + r * S::LD + col) = vv[u];
+            }
         }
         const bool masked = base + kBN > masked_from || base + kBN > keys;
         const bool select = __syncthreads_or(odd) && masked;
@@ -144,7 +154,7 @@ __device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float 
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 2
-        for (int k = 0; k < D; k += 4) {
+        for (int k = 0; k < D && busy; k += 4) {
             float4 kf[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) kf[j] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * j) * S::LD + k);
@@ -161,6 +171,7 @@ __device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float 
             }
         }
         __syncthreads();   // K has been read: P may take its place
+        if (!busy) continue;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float top = -INFINITY;
@@ -269,7 +280,9 @@ __device__ __forceinline__ void write_rows(const ServeArgs &a, const Work &w, co
     }
 }
 
-// Block b: key head b mod kv_heads of the (b / kv_heads)-th 64-row tile, the tiles counted over the sequences.
+// Block b: key head b mod kv_heads of the (b / kv_heads)-th 64-row tile. The tiles are numbered by falling position in
+// their sequence (the expensive ones start first), then by sequence: with N(p) = sum over the sequences of
+// max(0, tiles - p), tile t has the position p with N(p + 1) <= t < N(p), found by bisection.
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const ServeArgs a) {
     extern __shared__ __align__(16) float sm[];
@@ -279,41 +292,53 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const ServeArgs a
     const int64_t want = blockIdx.x / a.kv_heads;
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        int64_t run = 0;
-        int found = -1, tile = 0;
         bool ok = true;
-        for (int b = 0; b < a.seqs; b += 32) {
+        int one = 0;   // tiles of sequence `lane`, where there are no more than 32
+        auto tiles_of = [&](int s) -> int {
             int start = 0, len = 0;
-            if (b + lane < a.seqs) ok &= prompt_seq(a, b + lane, &start, &len);
-            const int64_t mine = (static_cast<int64_t>(len) * a.group + kBM - 1) / kBM;
-            int64_t sum = mine;
+            if (s < a.seqs) ok &= prompt_seq(a, s, &start, &len);
+            return static_cast<int>((static_cast<int64_t>(len) * a.group + kBM - 1) / kBM);
+        };
+        if (a.seqs <= 32) one = tiles_of(lane);
+        auto from = [&](int p) -> int64_t {   // N(p)
+            int64_t n = 0;
+            for (int b = 0; b < a.seqs; b += 32) {
+                const int t = a.seqs <= 32 ? one : tiles_of(b + lane);
+                n += t > p ? t - p : 0;
+            }
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t z = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += z;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, run + sum > want);
-            if (found < 0 && hit) {
-                const int s = __ffs(hit) - 1;
-                found = b + s;
-                tile = static_cast<int>(want - run - __shfl_sync(0xffffffffu, sum - mine, s));
-            }
-            run += __shfl_sync(0xffffffffu, sum, 31);
-            if (found >= 0 && blockIdx.x != 0) break;   // block 0 looks all sequences over
-        }
+            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            return n;
+        };
+        const int64_t all = from(0);
         if (!ok && blockIdx.x == 0) atomicOr(a.status, kStatusData);
+        int found = -1, p = 0;
+        if (want < all) {
+            int lo = 0, hi = static_cast<int>((static_cast<int64_t>(a.max_len) * a.group + kBM - 1) / kBM);   // N(hi) = 0 <= want
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (from(mid) > want) lo = mid;
+                else hi = mid;
+            }
+            p = lo;
+            int64_t at = from(p + 1);
+            for (int b = 0; b < a.seqs && found < 0; b += 32) {
+                const int t = a.seqs <= 32 ? one : tiles_of(b + lane);
+                const unsigned has = __ballot_sync(0xffffffffu, t > p);
+                if (want - at < __popc(has)) found = b + __fns(has, 0, static_cast<int>(want - at) + 1);
+                at += __popc(has);
+            }
+        }
         if (lane == 0) {
             Work w{};
             w.rows = 0;
             if (found >= 0) {
                 int start, len;
                 prompt_seq(a, found, &start, &len);
-                // a sequence's last (most expensive) tile first
-                const int tiles = static_cast<int>((static_cast<int64_t>(len) * a.group + kBM - 1) / kBM);
                 w.start = start;
                 w.t = len;
                 w.len = 0;
-                w.row0 = (tiles - 1 - tile) * kBM;
+                w.row0 = p * kBM;
                 w.rows = min(kBM, len * a.group - w.row0);
                 w.kh = kh;
                 w.k0 = 0;
