@@ -117,11 +117,11 @@ __device__ __forceinline__ float *tree_slot(void *ws, int blocks, int slot, int 
 // flattened rows, tok_tile 0) or whole tokens (tok_tile tokens).
 struct TreeWalk {
     int64_t total;         // key tiles of the call
+    int64_t per_head;      // of one key head
     int shares;            // blocks that get some: no share is empty, so a segment's pieces are in neighbouring blocks
-    int64_t first, last;   // this block's, in the segments' numbering
-    int64_t at;            // next one
-    int seq;               // sequence of `at`
-    int64_t seq_first;     // number of its first key tile
+    int64_t at, last;      // this block's next one and the one behind its last
+    int kh, seq;           // key head and sequence of `at`
+    int64_t seq_first;     // number of the sequence's first key tile
     TreeSeq x;
     TreeSeq lane_seq;      // sequence `lane` where the call has at most 32: each is read once
     int nk, tiles;
@@ -129,34 +129,37 @@ struct TreeWalk {
     static __device__ __forceinline__ int tiles_of(const ServeArgs &a, const TreeSeq &x, int tile_rows, int tok_tile) {
         return tok_tile ? (x.t + tok_tile - 1) / tok_tile : (x.t * a.group + tile_rows - 1) / tile_rows;
     }
+    // key tiles of a sequence for one key head
     static __device__ __forceinline__ int64_t cost(const ServeArgs &a, const TreeSeq &x, int key_tile, int tile_rows,
                                                    int tok_tile) {
         if (x.t == 0) return 0;
-        return static_cast<int64_t>(a.kv_heads) * tiles_of(a, x, tile_rows, tok_tile) *
-               ((x.len + x.t + key_tile - 1) / key_tile);
+        return static_cast<int64_t>(tiles_of(a, x, tile_rows, tok_tile)) * ((x.len + x.t + key_tile - 1) / key_tile);
     }
     __device__ __forceinline__ void begin(const ServeArgs &a, int key_tile, int tile_rows, int tok_tile, int block,
                                           int blocks) {
         const int lane = threadIdx.x & 31;
-        total = 0;
+        per_head = 0;
         bool ok = true;
         for (int b = 0; b < a.seqs; b += 32) {
             TreeSeq y;
             y.t = 0;
             if (b + lane < a.seqs) ok &= tree_seq(a, b + lane, &y);
-            total += cost(a, y, key_tile, tile_rows, tok_tile);
+            per_head += cost(a, y, key_tile, tile_rows, tok_tile);
             lane_seq = y;
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        for (int o = 16; o > 0; o >>= 1) per_head += __shfl_xor_sync(0xffffffffu, per_head, o);
         if (!ok && block == 0) atomicOr(a.status, kStatusData);
+        total = per_head * a.kv_heads;
         shares = static_cast<int>(min(total, static_cast<int64_t>(blocks)));
-        first = block < shares ? total * block / shares : 0;
+        at = block < shares ? total * block / shares : 0;
         last = block < shares ? total * (block + 1) / shares : 0;
-        at = first;
+        kh = 0;
         seq = a.seqs;
         seq_first = 0;
-        if (first == last) return;
+        if (at == last) return;
+        kh = static_cast<int>(at / per_head);
+        const int64_t first = at - kh * per_head;
         // the sequence that holds `first`
         int64_t run = 0;
         for (int b = 0; b < a.seqs; b += 32) {
@@ -176,7 +179,7 @@ struct TreeWalk {
             if (hit) {
                 const int l = __ffs(hit) - 1;
                 seq = b + l;
-                seq_first = run + __shfl_sync(0xffffffffu, sum - mine, l);
+                seq_first = kh * per_head + run + __shfl_sync(0xffffffffu, sum - mine, l);
                 break;
             }
             run += __shfl_sync(0xffffffffu, sum, 31);
@@ -195,14 +198,17 @@ struct TreeWalk {
         nk = x.t ? (x.len + x.t + key_tile - 1) / key_tile : 0;
         tiles = tiles_of(a, x, tile_rows, tok_tile);
     }
-    // The next piece of the share; false at its end. Row tiles vary fastest, then key heads: segments that read the
-    // same keys are neighbours.
+    // The next piece of the share; false at its end. Key heads vary slowest: the blocks of different heads go through
+    // the sequences at the same pace, so the heads' parts of a page, which lie together, are read at about the same time.
+    // Row tiles of the same keys are neighbours.
     __device__ __forceinline__ bool next(const ServeArgs &a, int key_tile, int tile_rows, int tok_tile, TreePiece *p) {
         if (at >= last) return false;
-        while (at - seq_first >= static_cast<int64_t>(a.kv_heads) * tiles * nk) {
-            seq_first += static_cast<int64_t>(a.kv_heads) * tiles * nk;
-            ++seq;
-            if (seq >= a.seqs) return false;
+        while (at - seq_first >= static_cast<int64_t>(tiles) * nk) {
+            seq_first += static_cast<int64_t>(tiles) * nk;
+            if (++seq >= a.seqs) {
+                seq = 0;
+                ++kh;
+            }
             load(a, key_tile, tile_rows, tok_tile);
         }
         const int64_t off = at - seq_first;
@@ -210,8 +216,8 @@ struct TreeWalk {
         p->seq = seq;
         p->x = x;
         p->nk = nk;
-        p->tile = static_cast<int>(segment % tiles);
-        p->kh = static_cast<int>(segment / tiles);
+        p->tile = static_cast<int>(segment);
+        p->kh = kh;
         p->k0 = static_cast<int>(off - segment * nk);
         const int64_t left = last - at;
         p->k1 = static_cast<int>(min(static_cast<int64_t>(nk), p->k0 + left));
