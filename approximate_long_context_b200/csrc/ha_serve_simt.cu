@@ -4,9 +4,10 @@
 //
 // One block: 64 query rows (row = token * group + head within its key head) against 64 keys at a time, one online
 // softmax: m' = max(m, max_j x_j), l' = l 2^(m - m') + sum_j 2^(x_j - m'), O' = O 2^(m - m') + sum_j 2^(x_j - m') v_j with
-// x_j = scale log2(e) q.k_j; O = O / l, L = (m + log2 l) ln 2. 128 threads, 8 rows x 4 keys each for the scores and
-// 8 rows x d/16 columns for the product with V: 12 (16) 16-byte shared loads feed 128 (256) fused multiply-adds, so the
-// FP32 pipes and not shared memory bound it. Sums, maxima and numerators are fp32.
+// x_j = scale log2(e) q.k_j; O = O / l, L = (m + log2 l) ln 2. 256 threads, 4 rows x 4 keys each for the scores and
+// 4 rows x d/16 columns for the product with V, in packed f32x2 instructions (pairs along d for the scores, so that the
+// 16-byte shared loads feed them as they are; pairs of columns for the product): 8 loads for 64 multiply-adds of 32
+// lanes. Sums, maxima and numerators are fp32.
 //
 // A value row of a masked key can hold an infinity or NaN and must not reach the rows that do not see it (0 * inf):
 // the load of a tile votes on non-finite values, and a tile with one and a mask takes the product with a select.
@@ -21,7 +22,7 @@
 namespace ha {
 namespace {
 
-constexpr int kBM = 64, kBN = 64, kThreads = 128;
+constexpr int kBM = 64, kBN = 64, kThreads = 256;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -64,14 +65,14 @@ struct Work {
 };
 
 template <int D, bool TREE, typename T>
-__device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float *sm, float (&acc)[8][D / 16], float (&m)[8],
-                                       float (&l)[8]) {
+__device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float *sm, float (&acc)[4][D / 16], float (&m)[4],
+                                       float (&l)[4]) {
     using S = Smem<D>;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     float *Qs = sm + S::kQ, *Ks = sm + S::kK, *Ps = Ks, *Vs = sm + S::kV;
     const float c = a.scale * kLog2e;
     const T *q = static_cast<const T *>(a.q);
-    const bool busy = (tid >> 5) * 16 < w.rows;   // some row of the warp
+    const bool busy = (tid >> 5) * 8 < w.rows;   // some row of the warp
     __syncthreads();   // the previous piece's reads are done
     for (int x = tid; x < kBM * (D / 4); x += kThreads) {
         const int r = x / (D / 4), col = (x % (D / 4)) * 4;
@@ -83,17 +84,17 @@ __device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float 
         *reinterpret_cast<float4 *>(Qs + r * S::LD + col) = v;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) acc[i][j] = 0.f;
     }
-    int tok[8];
-    uint64_t bits[8];
+    int tok[4];
+    uint64_t bits[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = min(w.rows - 1, ty * 8 + i);
+    for (int i = 0; i < 4; ++i) {
+        const int r = min(w.rows - 1, ty * 4 + i);
         tok[i] = (w.row0 + r) / a.group;
         bits[i] = TREE ? tree_bits(a, w.start, tok[i], w.t) : 0;
     }
@@ -148,32 +149,36 @@ __device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float 
         }
         const bool masked = base + kBN > masked_from || base + kBN > keys;
         const bool select = __syncthreads_or(odd) && masked;
-        float s[8][4];
+        // two partial sums per score, over the even and the odd of the d products, in packed instructions
+        uint64_t s2[4][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 2
+            for (int j = 0; j < 4; ++j) s2[i][j] = 0;
+#pragma unroll 4
         for (int k = 0; k < D && busy; k += 4) {
-            float4 kf[4];
+            ulonglong2 kf[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) kf[j] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * j) * S::LD + k);
+            for (int j = 0; j < 4; ++j) kf[j] = *reinterpret_cast<const ulonglong2 *>(Ks + (tx + 16 * j) * S::LD + k);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 qf = *reinterpret_cast<const float4 *>(Qs + (ty * 8 + i) * S::LD + k);
+            for (int i = 0; i < 4; ++i) {
+                const ulonglong2 qf = *reinterpret_cast<const ulonglong2 *>(Qs + (ty * 4 + i) * S::LD + k);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[i][j] = fmaf(qf.x, kf[j].x, s[i][j]);
-                    s[i][j] = fmaf(qf.y, kf[j].y, s[i][j]);
-                    s[i][j] = fmaf(qf.z, kf[j].z, s[i][j]);
-                    s[i][j] = fmaf(qf.w, kf[j].w, s[i][j]);
-                }
+                for (int j = 0; j < 4; ++j) s2[i][j] = f2_fma(qf.y, kf[j].y, f2_fma(qf.x, kf[j].x, s2[i][j]));
             }
         }
+        float s[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 v = f2_unpack(s2[i][j]);
+                s[i][j] = v.x + v.y;
+            }
         __syncthreads();   // K has been read: P may take its place
         if (!busy) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             float top = -INFINITY;
             unsigned seen = 0;
 #pragma unroll
@@ -197,7 +202,7 @@ __device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float 
             for (int j = 0; j < 4; ++j) {
                 const float p = seen >> j & 1 ? exp2f(s[i][j] - ref) : 0.f;
                 sum += p;
-                Ps[(ty * 8 + i) * S::LP + tx + 16 * j] = p;
+                Ps[(ty * 4 + i) * S::LP + tx + 16 * j] = p;
             }
             l[i] = l[i] * corr + sum;
 #pragma unroll
@@ -205,31 +210,36 @@ __device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float 
         }
         __syncwarp();   // a row's P is written and read by the same half warp
         if (!select) {
-#pragma unroll 1
+#pragma unroll 2
             for (int k = 0; k < kBN; k += 4) {
-                float4 p[8];
+                float4 p[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] = *reinterpret_cast<const float4 *>(Ps + (ty * 8 + i) * S::LP + k);
+                for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(Ps + (ty * 4 + i) * S::LP + k);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
+                for (int kk = 0; kk < 4; ++kk) {
+                    uint64_t pp[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float pk = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                        pp[i] = f2_pack(pk, pk);
+                    }
 #pragma unroll
                     for (int g = 0; g < D / 64; ++g) {
-                        const float4 v = *reinterpret_cast<const float4 *>(Vs + (k + kk) * S::LD + g * 64 + tx * 4);
+                        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(Vs + (k + kk) * S::LD + g * 64 + tx * 4);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float pk = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
-                            acc[i][g * 4 + 0] = fmaf(pk, v.x, acc[i][g * 4 + 0]);
-                            acc[i][g * 4 + 1] = fmaf(pk, v.y, acc[i][g * 4 + 1]);
-                            acc[i][g * 4 + 2] = fmaf(pk, v.z, acc[i][g * 4 + 2]);
-                            acc[i][g * 4 + 3] = fmaf(pk, v.w, acc[i][g * 4 + 3]);
+                        for (int i = 0; i < 4; ++i) {
+                            uint64_t *o = reinterpret_cast<uint64_t *>(&acc[i][g * 4]);
+                            o[0] = f2_fma(pp[i], v.x, o[0]);
+                            o[1] = f2_fma(pp[i], v.y, o[1]);
                         }
                     }
+                }
             }
         } else {
             for (int k = 0; k < kBN; ++k)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float pk = Ps[(ty * 8 + i) * S::LP + k];
+                for (int i = 0; i < 4; ++i) {
+                    const float pk = Ps[(ty * 4 + i) * S::LP + k];
 #pragma unroll
                     for (int g = 0; g < D / 64; ++g)
 #pragma unroll
@@ -241,19 +251,19 @@ __device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float 
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
 }
 
 // O = numerator / sum; a row that sees nothing (sum 0) is 0 with L = -inf.
 template <int D>
-__device__ __forceinline__ void write_rows(const ServeArgs &a, const Work &w, const float (&acc)[8][D / 16],
-                                           const float (&m)[8], const float (&l)[8]) {
+__device__ __forceinline__ void write_rows(const ServeArgs &a, const Work &w, const float (&acc)[4][D / 16],
+                                           const float (&m)[4], const float (&l)[4]) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = ty * 8 + i;
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty * 4 + i;
         if (r >= w.rows) continue;
         const int row = w.row0 + r, tok = row / a.group, head = w.kh * a.group + row - tok * a.group;
         const int64_t at = static_cast<int64_t>(w.start + tok) * a.o_tok + static_cast<int64_t>(head) * a.o_head;
@@ -284,7 +294,7 @@ __device__ __forceinline__ void write_rows(const ServeArgs &a, const Work &w, co
 // their sequence (the expensive ones start first), then by sequence: with N(p) = sum over the sequences of
 // max(0, tiles - p), tile t has the position p with N(p + 1) <= t < N(p), found by bisection.
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const ServeArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const ServeArgs a) {
     extern __shared__ __align__(16) float sm[];
     __shared__ Work shared;
     grid_dependency_wait();
@@ -350,13 +360,13 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const ServeArgs a
     __syncthreads();
     const Work w = shared;
     if (w.rows <= 0) return;
-    float acc[8][D / 16], m[8], l[8];
+    float acc[4][D / 16], m[4], l[4];
     attend<D, false, T>(a, w, sm, acc, m, l);
     write_rows<D>(a, w, acc, m, l);
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) tree_simt_kernel(const ServeArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const ServeArgs a) {
     extern __shared__ __align__(16) float sm[];
     __shared__ TreePiece piece;
     __shared__ int more;
@@ -387,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const ServeArgs a) 
         w.kh = piece.kh;
         w.k0 = piece.k0;
         w.k1 = piece.k1;
-        float acc[8][D / 16], m[8], l[8];
+        float acc[4][D / 16], m[4], l[4];
         attend<D, true, T>(a, w, sm, acc, m, l);
         if (piece.k0 == 0 && piece.k1 == piece.nk) {
             write_rows<D>(a, w, acc, m, l);
@@ -396,8 +406,8 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const ServeArgs a) 
         const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
         float *slot = tree_slot(a.ws, blocks, 2 * block + (piece.k0 == 0), kBM, D);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = ty * 8 + i;
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty * 4 + i;
             if (r >= w.rows) continue;
 #pragma unroll
             for (int g = 0; g < D / 64; ++g)
