@@ -156,9 +156,10 @@ struct ServeArgs {
     int sms;
 };
 
-size_t serve_prompt_workspace(int64_t tokens, int64_t seqs, int64_t max_len, int kv_heads, int group, int sms);
+size_t serve_prompt_workspace(bool tc, int64_t tokens, int64_t seqs, int64_t max_len, int kv_heads, int group, int sms);
+size_t prompt_tc_workspace(int64_t tokens, int64_t seqs, int64_t max_len, int kv_heads, int group, int sms);
 size_t serve_tree_workspace(int sms, int d);
-// Return the number of kernels launched, -1 on a launch error.
+// Return the number of kernels launched, -1 on a launch error, -2 for sizes that the kernels do not take.
 int launch_prompt_simt(const ServeArgs &a, int dtype, cudaStream_t st);
 int launch_tree_simt(const ServeArgs &a, int dtype, cudaStream_t st);
 int launch_prompt_tc(const ServeArgs &a, cudaStream_t st);

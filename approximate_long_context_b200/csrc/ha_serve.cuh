@@ -55,6 +55,17 @@ __device__ __forceinline__ bool prompt_seq(const ServeArgs &a, int i, int *start
     return ok;
 }
 
+// The list of a prompt call's items (sequence, index of its group of rows), in the workspace.
+struct PromptPlan {
+    int count;     // entries
+    int single;    // of them, at the end: sequences of one query tile, whose items take two key heads at a time
+    int pad[2];
+};
+int64_t prompt_items(int64_t tokens, int64_t seqs, int64_t rows, int group);
+size_t prompt_plan_bytes(int64_t items);
+// rows: query rows of an entry (token * group + head); singles_last: sequences of at most rows / 2 come last.
+bool launch_prompt_plan(const ServeArgs &a, int64_t rows, bool singles_last, int64_t items, cudaStream_t st);
+
 // Sequence i of a tree call: first query row, drafted rows t, committed rows len, its row of the page table. t = 0
 // (and a flag) where something is out of range.
 struct TreeSeq {
@@ -64,20 +75,16 @@ struct TreeSeq {
 __device__ __forceinline__ bool tree_seq(const ServeArgs &a, int i, TreeSeq *x) {
     const int64_t s = a.cu[i], e = a.cu[i + 1];
     const int64_t slot = a.slots ? a.slots[i] : i;
-    x->start = 0;
-    x->t = 0;
-    x->len = 0;
-    x->table = 0;
-    if (s < 0 || e < s || e > a.tokens || e - s > a.max_len || slot < 0 || slot >= a.max_slots) return false;
-    if (e == s) return true;
-    const int64_t len = a.lens[slot], held = a.held[slot];
-    if (len < 0 || held > a.max_pages || ((len + (e - s) + (int64_t(1) << a.page_shift) - 1) >> a.page_shift) > held)
-        return false;
-    x->start = static_cast<int>(s);
-    x->t = static_cast<int>(e - s);
-    x->len = static_cast<int>(len);
-    x->table = slot * a.max_pages;
-    return true;
+    bool ok = s >= 0 && e >= s && e <= a.tokens && e - s <= a.max_len && slot >= 0 && slot < a.max_slots;
+    const int64_t in = ok ? slot : 0;   // loads without a branch: several sequences' are in flight at a time
+    const int64_t len = a.lens[in], held = a.held[in];
+    const int64_t t = ok ? e - s : 0;
+    if (t > 0) ok = len >= 0 && held <= a.max_pages && ((len + t + (int64_t(1) << a.page_shift) - 1) >> a.page_shift) <= held;
+    x->start = ok ? static_cast<int>(s) : 0;
+    x->t = ok ? static_cast<int>(t) : 0;
+    x->len = ok ? static_cast<int>(len) : 0;
+    x->table = in * a.max_pages;
+    return ok;
 }
 
 // A contiguous run of key tiles of one segment (a sequence, a key head and a tile of query rows) that one block works
@@ -140,6 +147,7 @@ struct TreeWalk {
         const int lane = threadIdx.x & 31;
         per_head = 0;
         bool ok = true;
+#pragma unroll 4
         for (int b = 0; b < a.seqs; b += 32) {
             TreeSeq y;
             y.t = 0;

@@ -76,13 +76,13 @@ int check_cache(hyper_attn_t h, const ha_cache *c, ha::ServeCache *out) {
     return HA_OK;
 }
 
-int check_count(hyper_attn_t h, int64_t n) {
-    if (n < 0 || n > 65536) return fail(h, HA_ERR_INVALID_ARG, "n must lie in [0, 65536] (got %lld)", (long long)n);
+int check_count(hyper_attn_t h, int64_t n, int64_t most = 16384) {
+    if (n < 0 || n > most) return fail(h, HA_ERR_INVALID_ARG, "n must lie in [0, %lld] (got %lld)", (long long)most, (long long)n);
     return HA_OK;
 }
 
 int launched(hyper_attn_t h, int k, const char *what) {
-    if (k == -2) return fail(h, HA_ERR_UNSUPPORTED, "%s: too many tiles for one call", what);
+    if (k == -2) return fail(h, HA_ERR_UNSUPPORTED, "%s: sizes or strides that this kernel does not take", what);
     if (k < 0) return fail(h, HA_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(cudaGetLastError()));
     h->last_launches = k;
     return HA_OK;
@@ -103,7 +103,8 @@ int hyper_attn_capturing(hyper_attn_t h) {
 
 size_t hyper_attn_prompt_workspace(hyper_attn_t h, int64_t tokens, int64_t seqs, int64_t max_len, int heads, int kv_heads) {
     if (!h || tokens < 0 || seqs < 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads) return 0;
-    return ha::serve_prompt_workspace(tokens, seqs, max_len, kv_heads, heads / kv_heads, h->sms);
+    const bool tc = h->opt.kernel != HA_KERNEL_SIMT && h->opt.dtype == HA_DTYPE_BF16;
+    return ha::serve_prompt_workspace(tc, tokens, seqs, max_len, kv_heads, heads / kv_heads, h->sms);
 }
 
 int hyper_attn_prompt(hyper_attn_t h, const ha_prompt_args *p) {
@@ -133,7 +134,7 @@ int hyper_attn_prompt(hyper_attn_t h, const ha_prompt_args *p) {
         if ((rc = check_strides(h, "v", p->tokens, p->kv_heads, p->d, ei, &a.v_tok, &a.v_head, false))) return rc;
         if ((rc = check_strides(h, "o", p->tokens, p->heads, p->d, eo, &a.o_tok, &a.o_head, true))) return rc;
         if (p->o == p->q || p->o == p->k || p->o == p->v) return fail(h, HA_ERR_INVALID_ARG, "O must not alias Q, K or V");
-        const size_t need = ha::serve_prompt_workspace(p->tokens, p->seqs, p->max_len, p->kv_heads, p->heads / p->kv_heads, h->sms);
+        const size_t need = ha::serve_prompt_workspace(tc, p->tokens, p->seqs, p->max_len, p->kv_heads, p->heads / p->kv_heads, h->sms);
         if (need && (!p->workspace || !aligned16(p->workspace) || p->workspace_bytes < need))
             return fail(h, HA_ERR_INVALID_ARG, "workspace of %zu bytes needed, 16-byte aligned", need);
         a.tokens = p->tokens;
@@ -280,7 +281,7 @@ int hyper_attn_cache_append(hyper_attn_t h, const ha_cache *cache, const int32_t
     return guarded(h, [&]() -> int {
         ha::ServeCache c;
         int rc = check_cache(h, cache, &c);
-        if (rc || (rc = check_count(h, n))) return rc;
+        if (rc || (rc = check_count(h, n, 1 << 20))) return rc;
         if (tokens < 0 || tokens > kMaxTokens) return fail(h, HA_ERR_INVALID_ARG, "tokens must lie in [0, 2^30]");
         if (layer < 0 || layers < 1 || layer > c.layers - layers) return fail(h, HA_ERR_INVALID_ARG, "layers out of range");
         h->last_launches = 0;

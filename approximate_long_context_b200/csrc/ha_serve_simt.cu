@@ -291,10 +291,11 @@ __device__ __forceinline__ void write_rows(const ServeArgs &a, const Work &w, co
 }
 
 // Block b: key head b mod kv_heads of the (b / kv_heads)-th 64-row tile. The tiles are numbered by falling position in
-// their sequence (the expensive ones start first), then by sequence: with N(p) = sum over the sequences of
-// max(0, tiles - p), tile t has the position p with N(p + 1) <= t < N(p), found by bisection.
+// their sequence (the expensive ones start first). Up to 32 sequences the block finds its tile itself: with N(p) = sum over
+// the sequences of max(0, tiles - p), tile t has the position p with N(p + 1) <= t < N(p), found by bisection. Beyond that
+// the tiles come from a list.
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const ServeArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const ServeArgs a, bool listed) {
     extern __shared__ __align__(16) float sm[];
     __shared__ Work shared;
     grid_dependency_wait();
@@ -302,41 +303,35 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const ServeArg
     const int64_t want = blockIdx.x / a.kv_heads;
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        bool ok = true;
-        int one = 0;   // tiles of sequence `lane`, where there are no more than 32
-        auto tiles_of = [&](int s) -> int {
-            int start = 0, len = 0;
-            if (s < a.seqs) ok &= prompt_seq(a, s, &start, &len);
-            return static_cast<int>((static_cast<int64_t>(len) * a.group + kBM - 1) / kBM);
-        };
-        if (a.seqs <= 32) one = tiles_of(lane);
-        auto from = [&](int p) -> int64_t {   // N(p)
-            int64_t n = 0;
-            for (int b = 0; b < a.seqs; b += 32) {
-                const int t = a.seqs <= 32 ? one : tiles_of(b + lane);
-                n += t > p ? t - p : 0;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-            return n;
-        };
-        const int64_t all = from(0);
-        if (!ok && blockIdx.x == 0) atomicOr(a.status, kStatusData);
         int found = -1, p = 0;
-        if (want < all) {
-            int lo = 0, hi = static_cast<int>((static_cast<int64_t>(a.max_len) * a.group + kBM - 1) / kBM);   // N(hi) = 0 <= want
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (from(mid) > want) lo = mid;
-                else hi = mid;
+        if (listed) {
+            const PromptPlan *plan = static_cast<const PromptPlan *>(a.ws);
+            if (want < plan->count) {
+                const int2 e = reinterpret_cast<const int2 *>(plan + 1)[want];
+                found = e.x;
+                p = e.y;
             }
-            p = lo;
-            int64_t at = from(p + 1);
-            for (int b = 0; b < a.seqs && found < 0; b += 32) {
-                const int t = a.seqs <= 32 ? one : tiles_of(b + lane);
-                const unsigned has = __ballot_sync(0xffffffffu, t > p);
-                if (want - at < __popc(has)) found = b + __fns(has, 0, static_cast<int>(want - at) + 1);
-                at += __popc(has);
+        } else {
+            int start = 0, len = 0;
+            const bool ok = lane >= a.seqs || prompt_seq(a, lane, &start, &len);
+            if (!ok && blockIdx.x == 0) atomicOr(a.status, kStatusData);
+            const int tiles = static_cast<int>((static_cast<int64_t>(len) * a.group + kBM - 1) / kBM);
+            auto from = [&](int q) -> int64_t {   // N(q)
+                int64_t n = tiles > q ? tiles - q : 0;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+                return n;
+            };
+            if (want < from(0)) {
+                int lo = 0, hi = static_cast<int>((static_cast<int64_t>(a.max_len) * a.group + kBM - 1) / kBM);   // N(hi) = 0
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (from(mid) > want) lo = mid;
+                    else hi = mid;
+                }
+                p = lo;
+                const unsigned has = __ballot_sync(0xffffffffu, tiles > p);
+                found = __fns(has, 0, static_cast<int>(want - from(p + 1)) + 1);
             }
         }
         if (lane == 0) {
@@ -483,10 +478,13 @@ template <int D, typename T>
 int prompt_simt(const ServeArgs &a, cudaStream_t st) {
     static std::atomic<uint64_t> known{0};
     if (!allow_smem(prompt_simt_kernel<D, T>, Smem<D>::kBytes, &known)) return -1;
-    if ((a.tokens * a.group / kBM + a.seqs) * a.kv_heads > 0x7fffffff) return -2;   // blocks of a grid
-    const int64_t tiles = a.tokens * a.group / kBM + a.seqs;   // at most: one ragged tile per sequence
+    const int64_t tiles = prompt_items(a.tokens, a.seqs, kBM, a.group);
+    // blocks of a grid; row numbers within a sequence
+    if (tiles * a.kv_heads > 0x7fffffff || static_cast<int64_t>(a.max_len) * a.group > 0x7fffff00) return -2;
+    const bool listed = a.seqs > 32;
+    if (listed && !launch_prompt_plan(a, kBM, false, tiles, st)) return -1;
     const dim3 grid(static_cast<unsigned>(tiles * a.kv_heads));
-    return launch_dependent(prompt_simt_kernel<D, T>, grid, dim3(kThreads), Smem<D>::kBytes, st, a) ? 1 : -1;
+    return launch_dependent(prompt_simt_kernel<D, T>, grid, dim3(kThreads), Smem<D>::kBytes, st, a, listed) ? 1 + listed : -1;
 }
 
 template <int D, typename T>
@@ -505,6 +503,11 @@ bool launch_tree_join(const ServeArgs &a, int blocks, int rows, cudaStream_t st)
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((used + kJoinRows - 1) / kJoinRows));
     return a.d == 64 ? launch_dependent(tree_join_kernel<64>, grid, dim3(32 * kJoinRows), 0, st, a, blocks, rows)
                      : launch_dependent(tree_join_kernel<128>, grid, dim3(32 * kJoinRows), 0, st, a, blocks, rows);
+}
+
+size_t serve_prompt_workspace(bool tc, int64_t tokens, int64_t seqs, int64_t max_len, int kv_heads, int group, int sms) {
+    if (tc) return prompt_tc_workspace(tokens, seqs, max_len, kv_heads, group, sms);
+    return seqs > 32 ? prompt_plan_bytes(prompt_items(tokens, seqs, kBM, group)) : 0;
 }
 
 size_t serve_tree_workspace(int sms, int d) {

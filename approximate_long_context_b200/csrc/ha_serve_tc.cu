@@ -148,104 +148,6 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
 // tile take two key heads at a time (SINGLES).
 enum PromptOrder { SCAN = 0, LIST = 1, PAIRS = 2, SINGLES = 3 };
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanBuckets = 4096;
-
-struct PromptPlan {
-    int count;     // entries
-    int single;    // of them, at the end: sequences of one query tile, whose items take two key heads at a time
-    int pad[2];
-};
-
-__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const ServeArgs a, int pair_tokens, int capacity) {
-    grid_dependency_wait();
-    __shared__ int cursor[kPlanBuckets];
-    __shared__ int sums[32];
-    PromptPlan *head = static_cast<PromptPlan *>(a.ws);
-    int2 *list = reinterpret_cast<int2 *>(head + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int levels = (a.max_len + pair_tokens - 1) / pair_tokens;
-    int shift = 0;
-    while (((levels - 1) >> shift) + 2 > kPlanBuckets) ++shift;
-    const int buckets = ((levels - 1) >> shift) + 2;   // the last one: sequences of one query tile
-    // A lane reads a sequence; its pairs are handled by the lane itself, or by the whole warp if there are many. one(b, k)
-    // is called for k neighbouring entries of bucket b that belong to different lanes, many for one entry of a lane.
-    auto visit = [&](auto entry, bool report) {
-        bool ok = true;
-        for (int b = warp * 32; b < a.seqs; b += kPlanThreads) {
-            int start = 0, len = 0;
-            if (b + lane < a.seqs) ok &= prompt_seq(a, b + lane, &start, &len);
-            const int pairs = (len + pair_tokens - 1) / pair_tokens;
-            const bool single = len > 0 && 2 * len <= pair_tokens;
-            entry(single, buckets - 1, b + lane, 0);
-            const unsigned big = __ballot_sync(0xffffffffu, pairs > 4);
-            for (int p = 0; p < 4; ++p) {
-                const bool mine = !single && p < pairs && !(big >> lane & 1u);
-                if (__any_sync(0xffffffffu, mine)) entry(mine, buckets - 2 - (p >> shift), b + lane, p);
-            }
-            for (unsigned rest = big; rest; rest &= rest - 1) {
-                const int l = __ffs(rest) - 1, n = __shfl_sync(0xffffffffu, pairs, l);
-                for (int p0 = 0; p0 < n; p0 += 32) entry(p0 + lane < n, buckets - 2 - ((p0 + lane) >> shift), b + l, p0 + lane);
-            }
-        }
-        if (report && !ok) atomicOr(a.status, kStatusData);
-    };
-    // the place of an entry in its bucket; the lanes of a warp that meet in one bucket take their places with one addition
-    auto place = [&](bool mine, int b) -> int {
-        const unsigned same = __match_any_sync(0xffffffffu, mine ? b : -1);
-        const int leader = __ffs(same) - 1;
-        int at = 0;
-        if (mine && lane == leader) at = atomicAdd(&cursor[b], __popc(same));
-        return __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1u));
-    };
-    for (int b = tid; b < buckets; b += kPlanThreads) cursor[b] = 0;
-    __syncthreads();
-    visit([&](bool mine, int b, int, int) { place(mine, b); }, true);
-    __syncthreads();
-    const int singles = cursor[buckets - 1];
-    // exclusive sums over the buckets, highest position first: four buckets per thread
-    int mine[kPlanBuckets / kPlanThreads], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPlanBuckets / kPlanThreads; ++i) {
-        const int b = tid * (kPlanBuckets / kPlanThreads) + i;
-        mine[i] = sum;
-        sum += b < buckets ? cursor[b] : 0;
-    }
-    int x = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) sums[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int w = sums[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        sums[lane] = w;
-    }
-    __syncthreads();
-    const int before = x - sum + (warp ? sums[warp - 1] : 0);
-#pragma unroll
-    for (int i = 0; i < kPlanBuckets / kPlanThreads; ++i) {
-        const int b = tid * (kPlanBuckets / kPlanThreads) + i;
-        if (b < buckets) cursor[b] = before + mine[i];
-    }
-    if (tid == 0) {
-        head->count = min(sums[31], capacity);   // overlapping sequences (reported) could ask for more
-        head->single = max(0, singles - (sums[31] - head->count));
-    }
-    __syncthreads();
-    visit([&](bool mine, int b, int s, int p) {
-        const int at = place(mine, b);
-        if (mine && at < capacity) list[at] = make_int2(s, p);
-    }, false);
-}
-
 // The walk of one block over a prompt call's items, run by one whole warp.
 struct PromptWalk {
     int64_t count;    // items
@@ -259,11 +161,10 @@ struct PromptWalk {
         if (x.order >= PAIRS) {
             // the offsets are looked over here, as no list is made
             bool ok = true;
-            if (blockIdx.x == 0)
-                for (int b = lane; b < a.seqs; b += 32) {
-                    int start, len;
-                    ok &= prompt_seq(a, b, &start, &len);
-                }
+            for (int b = blockIdx.x * 32 + lane; b < a.seqs; b += gridDim.x * 32) {
+                int start, len;
+                ok &= prompt_seq(a, b, &start, &len);
+            }
             if (!ok) atomicOr(a.status, kStatusData);
             count = static_cast<int64_t>(a.seqs) * (x.order == SINGLES ? (a.kv_heads + 1) >> 1 : a.kv_heads);
             return;
@@ -1184,21 +1085,18 @@ bool launch(const TcArgs &x, const Maps &maps, int blocks, cudaStream_t st) {
     return launch_dependent(serve_tc_kernel<D, MODE>, dim3(blocks), dim3(kThreads), C::kBytes, st, x, maps);
 }
 
-// Items of a prompt call: every sequence has at most one pair of tiles that is not full.
-int64_t prompt_items(int64_t tokens, int64_t seqs, int tpt) { return tokens / (2 * tpt) + seqs; }
-
 // The list costs an extra launch (about 5 us) and is made only where the order of the items matters.
 int prompt_order(int64_t tokens, int64_t seqs, int64_t max_len, int kv_heads, int group, int sms) {
     const int tpt = 128 / group;
-    if (seqs <= 1 || prompt_items(tokens, seqs, tpt) * kv_heads <= sms) return SCAN;
+    if (seqs <= 1 || prompt_items(tokens, seqs, 2 * tpt * group, group) * kv_heads <= sms) return SCAN;
     return max_len <= tpt ? SINGLES : max_len <= 2 * tpt ? PAIRS : LIST;
 }
 
 }  // namespace
 
-size_t serve_prompt_workspace(int64_t tokens, int64_t seqs, int64_t max_len, int kv_heads, int group, int sms) {
+size_t prompt_tc_workspace(int64_t tokens, int64_t seqs, int64_t max_len, int kv_heads, int group, int sms) {
     if (group > 128 || prompt_order(tokens, seqs, max_len, kv_heads, group, sms) != LIST) return 0;
-    return sizeof(PromptPlan) + static_cast<size_t>(prompt_items(tokens, seqs, 128 / group)) * sizeof(int2);
+    return prompt_plan_bytes(prompt_items(tokens, seqs, 2 * (128 / group) * group, group));
 }
 
 int launch_prompt_tc(const ServeArgs &a, cudaStream_t st) {
@@ -1207,8 +1105,8 @@ int launch_prompt_tc(const ServeArgs &a, cudaStream_t st) {
     x.tpt = 128 / a.group;
     const int box_tokens = static_cast<int>(a.max_len < x.tpt ? a.max_len : x.tpt);
     x.box_rows = box_tokens * a.group;
-    const int64_t items = prompt_items(a.tokens, a.seqs, x.tpt);
-    if (items > 0x7fffffff) return -2;
+    const int64_t items = prompt_items(a.tokens, a.seqs, 2 * x.tpt * a.group, a.group);
+    if (items > 0x7fffffff || a.max_len > (1 << 26)) return -2;   // an item has to end well within the limit of a wait
     x.order = prompt_order(a.tokens, a.seqs, a.max_len, a.kv_heads, a.group, a.sms);
     Maps maps;
     if (!make_rows_map(&maps.q, a.q, a.d, a.heads, a.tokens, a.q_head, a.q_tok, a.group, box_tokens) ||
@@ -1216,8 +1114,7 @@ int launch_prompt_tc(const ServeArgs &a, cudaStream_t st) {
         !make_rows_map(&maps.v, a.v, a.d, a.kv_heads, a.tokens, a.v_head, a.v_tok, 1, 128))
         return -2;
     if (x.order == LIST) {
-        if (!launch_dependent(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, 2 * x.tpt, static_cast<int>(items)))
-            return -1;
+        if (!launch_prompt_plan(a, 2 * x.tpt * a.group, true, items, st)) return -1;
     }
     const int64_t most = items * a.kv_heads;
     const int blocks = static_cast<int>(most < a.sms ? most : a.sms);

@@ -329,7 +329,7 @@ typedef struct {
     int heads, kv_heads, d;
     const int32_t *offsets;           /* device, [seqs + 1], ascending: sequence s is rows offsets[s] .. offsets[s+1]-1 */
     int64_t seqs;                     /* <= 2^20; empty sequences are allowed */
-    int64_t max_len;                  /* no sequence is longer than this */
+    int64_t max_len;                  /* no sequence is longer than this; at most 2^26 on the tensor cores */
     float scale;
     void *workspace;                  /* hyper_attn_prompt_workspace bytes; 0 bytes: may be NULL */
     size_t workspace_bytes;
@@ -376,7 +376,7 @@ typedef struct {
 HA_API size_t hyper_attn_tree_workspace(hyper_attn_t h, int d);
 HA_API int hyper_attn_tree(hyper_attn_t h, const ha_cache *cache, const ha_tree_args *args);
 
-/* The cache's steps; n entries (n = 0: nothing is done), all lists in device memory. A slot named twice in one
+/* The cache's steps; n entries (n = 0: nothing is done; at most 16384, append 2^20), all lists in device memory. A slot named twice in one
  * call counts once (the first time) and is reported by hyper_attn_status like an entry out of range.
  *   free     releases the pages of slots[i] and empties the slot.
  *   fork     dst[i] (an empty slot) becomes a copy of src[i]: it shares the pages of the committed rows. Sources

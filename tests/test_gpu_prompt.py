@@ -74,6 +74,92 @@ def test_prompt_matches_definition(ha, kind, d, heads, lens):
     verify(q, k, v, O, lse, lens, d ** -0.5, UBF if kind in ("bf16", "bf16_to_fp32") else None, out_bf16)
 
 
+def random_lens(n, most, seed, empty=0.1):
+    import random
+    rng = random.Random(seed)
+    return [0 if rng.random() < empty else rng.randint(1, most) for _ in range(n)]
+
+
+MANY = {
+    # sequences, longest, key heads, group: all the ways in which a call's work is found and ordered
+    "list": (100, 400, 2, 2),
+    "list_shared_heads": (90, 300, 3, 7),
+    "pairs": (300, 60, 2, 4),
+    "singles": (400, 32, 2, 4),
+    "singles_odd_heads": (200, 120, 3, 1),
+    "few": (7, 200, 2, 1),
+    "no_head_room": (170, 9, 1, 128),
+    "thousands": (5000, 3, 1, 2),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", list(MANY), ids=list(MANY))
+def test_many_sequences(ha, dtype, case):
+    seqs, most, hk, group = MANY[case]
+    lens = random_lens(seqs, most, seed=seqs)
+    total, d = sum(lens), 64
+    q, k, v = make(total, hk * group, hk, d, dtype, seed=7)
+    options(ha, dtype)
+    O = torch.full_like(q, 7.0, device="cuda")
+    lse = torch.full((hk * group, total), 7.0, device="cuda")
+    cu = torch.tensor(offsets_of(lens), dtype=torch.int32, device="cuda")
+    ha.prompt(q.cuda(), k.cuda(), v.cuda(), O, cu, max_len=most, scale=0.125, lse=lse)
+    assert ha.status() == 0, ha.last_error()
+    o, l = O.cpu(), lse.cpu()
+    step = max(1, seqs // 150)          # all of them, or every so many
+    at = offsets_of(lens)
+    keep = [i for i in range(seqs) if i % step == 0 or i >= seqs - 3]
+    verify(q, k, v, o, l, [lens[i] for i in keep], 0.125, UBF if dtype == "bf16" else None, dtype == "bf16", at=[at[i] for i in keep])
+    assert not bool((o == 7).all(2).any()) and not bool((l == 7).any())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", ["list", "pairs", "singles", "few"])
+def test_bad_offsets_among_many(ha, dtype, case):
+    """One sequence longer than promised and one offset that falls back, among many: the others are right, those are left."""
+    seqs, most, hk, group = MANY[case]
+    lens = random_lens(seqs, most, seed=seqs, empty=0.0)
+    lens[3] = most + 1
+    total = sum(lens)
+    at = offsets_of(lens)
+    q, k, v = make(total, hk * group, hk, 64, dtype, seed=8)
+    options(ha, dtype)
+    O = torch.full_like(q, 7.0, device="cuda")
+    bad = list(at)
+    bad[seqs] = total + 1                # the last sequence ends behind the rows
+    ha.prompt(q.cuda(), k.cuda(), v.cuda(), O, torch.tensor(bad, dtype=torch.int32, device="cuda"), max_len=most, scale=0.125)
+    assert ha.status() == binding.HA_ERR_INVALID_ARG and ha.status() == 0
+    o = O.cpu()
+    assert bool((o[at[3]:at[4]] == 7).all()) and bool((o[at[seqs - 1]:] == 7).all())
+    good = [i for i in range(0, seqs - 1, max(1, seqs // 40)) if i != 3]
+    verify(q, k, v, o, None, [lens[i] for i in good], 0.125, UBF if dtype == "bf16" else None, dtype == "bf16", at=[at[i] for i in good])
+
+
+def test_two_handles_on_two_streams():
+    """Eager calls of two handles that overlap on the device."""
+    lens = random_lens(60, 500, seed=3)
+    total = sum(lens)
+    cu = torch.tensor(offsets_of(lens), dtype=torch.int32, device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    handles = [binding.HyperAttention(0) for _ in streams]
+    data = [make(total, 4, 2, 128, "bf16", seed=40 + i) for i in range(2)]
+    dev = [[x.cuda() for x in d] for d in data]
+    outs = [[torch.empty_like(d[0]) for _ in range(4)] for d in dev]
+    torch.cuda.synchronize()
+    for h, s in zip(handles, streams):
+        h.set_options(dtype="bf16", stream=s.cuda_stream)
+    for r in range(4):
+        for h, d, o in zip(handles, dev, outs):
+            h.prompt(*d, o[r], cu, max_len=500, scale=0.1)
+    for h, d, o in zip(handles, data, outs):
+        assert h.status() == 0, h.last_error()
+        for x in o[1:]:
+            assert torch.equal(o[0], x)
+        verify(*d, o[0], None, lens, 0.1, UBF, True)
+        h.close()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("group", [16, 100, 128])
 def test_many_query_heads_to_one_key_head(ha, dtype, group):

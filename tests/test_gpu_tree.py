@@ -154,6 +154,101 @@ def test_many_rows_to_one_key_head(ha, dtype, group, draft):
     verify(f, q, O, lse, lens, drafts, None, 0.125, UBF if dtype == "bf16" else None, dtype == "bf16")
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "bf16_to_fp32"])
+@pytest.mark.parametrize("draft", [1, 20])
+def test_many_sequences(ha, kind, draft):
+    """More sequences than a warp has lanes, some idle, one of them out of range; a slot that two sequences read."""
+    rng = random.Random(draft)
+    dtype, hk, group, d = kind[:4], 2, 8, 64
+    lens = [rng.choice([0, 1, 77, 128, 300, 1000]) for _ in range(110)]
+    drafts = [0 if rng.random() < 0.1 else rng.randint(1, draft) for _ in lens]
+    drafts[40] = drafts[41] = 1
+    f = Filled(lens, drafts, page=16, hk=hk, d=d, dtype=dtype, seed=draft)
+    slots = list(f.order)
+    slots[40] = slots[41]                       # both read slot 41's rows
+    slots[77] = 10 ** 6
+    lens[40], f.keys[40], f.values[40] = lens[41], f.keys[41], f.values[41]
+    drafts[77] = max(drafts[77], 1)
+    total = sum(drafts)
+    q = torch.randn(total, hk * group, d, generator=torch.Generator().manual_seed(1)).to(DT[dtype])
+    bf = kind == "bf16"
+    options(ha, dtype, out_dtype="fp32" if kind.endswith("to_fp32") else None)
+    O = torch.full(q.shape, 7.0, dtype=torch.bfloat16 if bf else torch.float32, device="cuda")
+    lse = torch.full((hk * group, total), 7.0, device="cuda")
+    ha.tree(q.cuda(), f.cache, O, ints(slots), ints(offsets_of(drafts)), max_draft=draft, layer=1, scale=0.125, lse=lse)
+    assert ha.status() == binding.HA_ERR_INVALID_ARG and ha.status() == 0
+    verify(f, q, O.cpu(), lse.cpu(), lens, drafts, None, 0.125, UBF if dtype == "bf16" else None, bf, skip=(77,))
+    a = offsets_of(drafts)
+    assert bool((O[a[77]:a[78]] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("group,draft", [(2, 5), (8, 64)])
+def test_not_finite_in_a_long_cache(ha, dtype, group, draft):
+    """A context cut over many blocks: infinities in a drafted row and in the last, partly masked tile of the context
+    reach the tokens that see them and no other."""
+    n, d = 6000, 128
+    f = Filled([n], [draft], page=64, hk=1, d=d, dtype=dtype, seed=5, order=[0])
+    masks = [1 << i for i in range(draft)]      # every token sees itself alone of the draft
+    at = n + 3
+    cache = f.cache
+    cache.v[1, cache.table[0, at // 64].item(), 0, at % 64, 9] = float("inf")
+    q = torch.randn(draft, group, d, generator=torch.Generator().manual_seed(2)).to(DT[dtype])
+    options(ha, dtype)
+    O = torch.empty_like(q, device="cuda")
+    call = lambda: ha.tree(q.cuda(), cache, O, None, ints([0, draft]), mask=signed(masks), max_draft=draft, layer=1, scale=0.09)  # noqa: E731
+    call()
+    assert ha.status() == 0, ha.last_error()
+    assert bool((O[3, :, 9].float() == float("inf")).all())
+    O[3, :, 9] = 0
+    assert bool(torch.isfinite(O).all())
+    f.values[0][at, 0, 9] = 0
+    keep = [i for i in range(draft) if i != 3]
+    seen = torch.ones(draft, n + draft, dtype=torch.bool)
+    seen[:, n:] = torch.eye(draft, dtype=torch.bool)
+    want = attend(q, f.keys[0], f.values[0], seen, 0.09)
+    tol = tolerances(*want, n + draft, d, p_bits=UBF if dtype == "bf16" else None, out_bf16=dtype == "bf16")
+    check(O.cpu()[keep], None, [want[0][keep], want[1]], [tol[0][keep], tol[1]])
+    at = n - 1                                  # the context's last row, in a masked tile: every token sees it
+    cache.v[1, cache.table[0, at // 64].item(), 0, at % 64, 11] = float("-inf")
+    call()
+    assert bool((O[:, :, 11].float() == float("-inf")).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_graphs_on_two_streams(ha, dtype):
+    """Two captured decode steps replayed at once on two streams, each with its own workspace."""
+    lens, drafts = [700, 3000, 64], [4, 1, 9]
+    total = sum(drafts)
+    state = []
+    for i in range(2):
+        s = torch.cuda.Stream()
+        f = Filled(lens, drafts, page=32, hk=2, d=64, dtype=dtype, seed=50 + i)
+        q = torch.randn(total, 8, 64, generator=torch.Generator().manual_seed(i)).to(DT[dtype])
+        Q, at, slots = q.cuda(), ints(offsets_of(drafts)), ints(f.order)
+        O = torch.empty_like(Q)
+        torch.cuda.synchronize()
+        ha.set_options(dtype=dtype, stream=s.cuda_stream)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(3):
+                ha.tree(Q, f.cache, O, slots, at, max_draft=9, layer=1, scale=0.125)
+        state.append((s, f, q, Q, O, g, at, slots))
+    options(ha, dtype)
+    for r in range(4):
+        for _, _, _, _, O, _, _, _ in state:
+            O.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for s, _, _, _, _, g, _, _ in state:
+            with torch.cuda.stream(s):
+                for _ in range(4):
+                    g.replay()
+        torch.cuda.synchronize()
+        for _, f, q, _, O, _, _, _ in state:
+            verify(f, q, O.cpu(), None, lens, drafts, None, 0.125, UBF if dtype == "bf16" else None, dtype == "bf16")
+    assert ha.status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_rows_that_see_nothing(ha, dtype):
     """Masks that leave drafted tokens of the context, and with an empty context nothing at all: 0 and -inf."""
@@ -489,6 +584,85 @@ def test_append_does_not_write_a_shared_page(ha):
     ha.cache_append(c, ints([1]), ints([0, 1]), row, row)
     assert ha.status() == 0 and c.k.sum().item() == 64
     assert c.table.tolist() == [[0, 1, -1], [0, 2, -1]]
+
+
+def test_empty_lists_and_graph_of_steps(ha):
+    """Lists of no entries do nothing; a captured cycle of all steps gives the same state at every replay."""
+    side = torch.cuda.Stream()
+    ha.set_options(dtype="bf16", stream=side.cuda_stream)
+    c = binding.PagedCache.empty(layers=2, pages=12, kv_heads=2, page=16, d=64, slots=3, max_pages=4)
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    row = torch.randn(2, 21, 2, 64, device="cuda").to(torch.bfloat16)
+    torch.cuda.synchronize()
+    ha.cache_free(c, none)
+    ha.cache_fork(c, none, none)
+    ha.cache_reserve(c, none, none)
+    ha.cache_append(c, none, ints([0]), row[:, :0], row[:, :0])
+    ha.cache_commit(c, none, none)
+    ha.cache_reserve(c, ints([0]), ints([21]))
+    ha.cache_append(c, ints([0]), ints([0, 21]), row, row)
+    ha.cache_commit(c, ints([0]), ints([21]))
+    assert ha.status() == 0, ha.last_error()
+    lists = dict(src=ints([0, 0]), dst=ints([2, 1]), add=ints([3, 14]), at=ints([0, 3, 17]), n=ints([2, 5]),
+                 keep=ints([[0, 2, -1, -1, -1], [1, 3, 4, 8, 13]]))
+    granted = ints([0, 0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        ha.cache_free(c, lists["dst"])
+        ha.cache_fork(c, lists["src"], lists["dst"])
+        ha.cache_reserve(c, lists["dst"], lists["add"], granted)
+        ha.cache_append(c, lists["dst"], lists["at"], row[:, :17], row[:, :17])
+        ha.cache_commit(c, lists["dst"], lists["n"], lists["keep"])
+    states = []
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            g.replay()
+        assert ha.status() == 0, ha.last_error()
+        states.append([x.clone() for x in (c.k, c.v, c.table, c.lens, c.held, c.refs, granted)])
+        torch.cuda.synchronize()
+    for s in states[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(states[0], s))
+    assert c.lens.tolist() == [21, 26, 23] and granted.tolist() == [3, 14]
+    rows = lambda slot, n: c.k[:, c.table[slot][:-(-n // 16)].long()].transpose(2, 3).flatten(1, 2)[:, :n]  # noqa: E731
+    assert torch.equal(rows(2, 23), torch.cat([row, row[:, [0, 2]]], 1))
+    assert torch.equal(rows(1, 26), torch.cat([row, row[:, [4, 6, 7, 11, 16]]], 1))
+    del g
+    options(ha, "bf16")
+
+
+def test_many_entries(ha):
+    """More entries than the planning block has threads: a shared page among them, and a pool that ends in between."""
+    n, pages = 1500, 1400
+    c = binding.PagedCache.empty(layers=1, pages=pages, kv_heads=1, page=16, d=64, slots=n, max_pages=2)
+    options(ha, "bf16")
+    ref = ListCache(bits(c.k).copy(), bits(c.v).copy(), n, 2)
+    row = torch.randn(1, 5, 1, 64).to(torch.bfloat16)
+    ha.cache_reserve(c, ints([7]), ints([5]))
+    ha.cache_append(c, ints([7]), ints([0, 5]), row.cuda(), row.cuda())
+    ha.cache_commit(c, ints([7]), ints([5]))
+    ref.reserve([7], [5])
+    ref.append([7], [0, 5], bits(row), bits(row))
+    ref.commit([7], [5])
+    dst = list(range(100, 1300))
+    ha.cache_fork(c, ints([7] * len(dst)), ints(dst))
+    ref.fork([7] * len(dst), dst)
+    who = list(range(n))[::-1]
+    add = [1 + (s % 3) * 8 for s in who]
+    granted = torch.zeros(n, dtype=torch.int32, device="cuda")
+    ha.cache_reserve(c, ints(who), ints(add), granted)
+    assert granted.tolist() == ref.reserve(who, add)
+    assert 0 < sum(g == 0 for g in granted.tolist()) < n
+    assert ha.status() == 0, ha.last_error()
+    same_state(c, ref)
+    assert np.array_equal(bits(c.k), ref.k)
+    counts = [min(1, g) for g in granted.tolist()]
+    ha.cache_commit(c, ints(who), ints(counts))
+    ref.commit(who, counts)
+    ha.cache_free(c, ints(who[:900]))
+    ref.free(who[:900])
+    assert ha.status() == 0, ha.last_error()
+    same_state(c, ref)
 
 
 def test_cache_refusals(ha):
