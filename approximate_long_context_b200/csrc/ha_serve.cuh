@@ -13,7 +13,17 @@ namespace ha {
 
 // A kernel launched with launch_dependent may start before the kernel in front of it on the stream has ended; it calls
 // this before it touches memory that the other one reads or writes (returns once that kernel and its writes are done).
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The kernel behind it may in turn start from here on, where it fits: its launch and set-up overlap with this one.
+__device__ __forceinline__ void grid_dependency_wait() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// a / b for 0 <= a, 0 < b: 64-bit division takes some hundred cycles, and nearly all values fit in 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
 
 // Launch behind the previous kernel of the stream without waiting for its last block to drain first (programmatic
 // stream serialisation); the kernel must call grid_dependency_wait. True on success.
@@ -160,13 +170,13 @@ struct TreeWalk {
         if (!ok && block == 0) atomicOr(a.status, kStatusData);
         total = per_head * a.kv_heads;
         shares = static_cast<int>(min(total, static_cast<int64_t>(blocks)));
-        at = block < shares ? total * block / shares : 0;
-        last = block < shares ? total * (block + 1) / shares : 0;
+        at = block < shares ? quotient(total * block, shares) : 0;
+        last = block < shares ? quotient(total * (block + 1), shares) : 0;
         kh = 0;
         seq = a.seqs;
         seq_first = 0;
         if (at == last) return;
-        kh = static_cast<int>(at / per_head);
+        kh = static_cast<int>(quotient(at, per_head));
         const int64_t first = at - kh * per_head;
         // the sequence that holds `first`
         int64_t run = 0;
@@ -220,7 +230,7 @@ struct TreeWalk {
             load(a, key_tile, tile_rows, tok_tile);
         }
         const int64_t off = at - seq_first;
-        const int64_t segment = off / nk;
+        const int64_t segment = quotient(off, nk);
         p->seq = seq;
         p->x = x;
         p->nk = nk;
@@ -240,7 +250,7 @@ struct TreeWalk {
 // Blocks that share the segment of which `p` (begun and not ended by `block`) is the first piece.
 __device__ __forceinline__ int tree_pieces(const TreePiece &p, int block) {
     int n = 1;   // the blocks behind it whose share begins before the segment's end
-    while (block + n < p.shares && p.total * (block + n) / p.shares < p.end) ++n;
+    while (block + n < p.shares && quotient(p.total * (block + n), p.shares) < p.end) ++n;
     return n;
 }
 

@@ -439,24 +439,48 @@ __global__ void __launch_bounds__(32 * kJoinRows) tree_join_kernel(const ServeAr
     auto slot_of = [&](int i) {
         return tree_slot(a.ws, blocks, i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i), rows, D);
     };
-    float m = -INFINITY;
-    for (int i = lane; i < j.pieces; i += 32) m = fmaxf(m, slot_of(i)[rows * D + r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float acc[C], l = 0.f;
+    // 32 pieces at a time: lane i has the maximum and the sum of piece i, all lanes its numerators, eight pieces in flight.
+    // The running result is brought to a new maximum as in the softmax itself.
+    float m = -INFINITY, l = 0.f, acc[C];
 #pragma unroll
     for (int e = 0; e < C; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < j.pieces; ++i) {
-        const float *s = slot_of(i);
-        const float w = exp2f(s[rows * D + r] - ref);
-        l += w * s[rows * (D + 1) + r];
-        float v[C];
-        if (C == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(s + r * D + lane * 4);
-        else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(s + r * D + lane * 2);
+    for (int first = 0; first < j.pieces; first += 32) {
+        const int n = min(32, j.pieces - first);
+        float mi = -INFINITY, li = 0.f;
+        if (lane < n) {
+            const float *s = slot_of(first + lane);
+            mi = s[rows * D + r];
+            li = s[rows * (D + 1) + r];
+        }
+        float top = mi;
 #pragma unroll
-        for (int e = 0; e < C; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+        const float back = exp2f(m - ref), w = exp2f(mi - ref);
+        m = mn;
+        float sum = w * li;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l = l * back + sum;
+#pragma unroll
+        for (int e = 0; e < C; ++e) acc[e] *= back;
+        for (int b = 0; b < n; b += 8) {
+            float v[8][C];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (b + u >= n) continue;
+                const float *s = slot_of(first + b + u) + r * D;
+                if (C == 4) *reinterpret_cast<float4 *>(v[u]) = *reinterpret_cast<const float4 *>(s + lane * 4);
+                else *reinterpret_cast<float2 *>(v[u]) = *reinterpret_cast<const float2 *>(s + lane * 2);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float wu = __shfl_sync(0xffffffffu, w, (b + u) & 31);
+                if (b + u >= n) continue;
+#pragma unroll
+                for (int e = 0; e < C; ++e) acc[e] = fmaf(wu, v[u][e], acc[e]);
+            }
+        }
     }
     const int row = j.row0 + r, tok = row / a.group, head = j.kh * a.group + row - tok * a.group;
     const int64_t at = static_cast<int64_t>(j.start + tok) * a.o_tok + static_cast<int64_t>(head) * a.o_head + lane * C;
@@ -471,7 +495,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) tree_join_kernel(const ServeAr
         for (int e = 0; e < C; ++e) static_cast<float *>(a.o)[at + e] = l == 0.f ? 0.f : acc[e] * inv;
     }
     if (a.lse && lane == 0)
-        a.lse[static_cast<int64_t>(head) * a.tokens + j.start + tok] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+        a.lse[static_cast<int64_t>(head) * a.tokens + j.start + tok] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <int D, typename T>

@@ -196,8 +196,9 @@ struct PromptWalk {
                 const int64_t i = round * gridDim.x + blockIdx.x;
                 if (i >= count) return false;
                 *single = x.order == SINGLES;
-                *seq = static_cast<int>(*single ? i / half : i / a.kv_heads);
-                *kh = *single ? 2 * static_cast<int>(i % half) : static_cast<int>(i % a.kv_heads);
+                const int per = *single ? half : a.kv_heads;
+                *seq = static_cast<int>(quotient(i, per));
+                *kh = static_cast<int>(i - static_cast<int64_t>(*seq) * per) * (*single ? 2 : 1);
                 *pair = 0;
                 int start, len;
                 prompt_seq(a, *seq, &start, &len);
@@ -213,15 +214,16 @@ struct PromptWalk {
         if (x.order == LIST) {
             const int half = (a.kv_heads + 1) >> 1;
             *single = i >= normal;
-            const int64_t at = *single ? normal / a.kv_heads + (i - normal) / half : i / a.kv_heads;
-            *kh = *single ? 2 * static_cast<int>((i - normal) % half) : static_cast<int>(i % a.kv_heads);
+            const int64_t own = *single ? i - normal : i, group = quotient(own, *single ? half : a.kv_heads);
+            const int64_t at = *single ? quotient(normal, a.kv_heads) + group : group;
+            *kh = static_cast<int>(own - group * (*single ? half : a.kv_heads)) * (*single ? 2 : 1);
             const int2 e = reinterpret_cast<const int2 *>(static_cast<const PromptPlan *>(a.ws) + 1)[at];
             *seq = e.x;
             *pair = e.y;
             return true;
         }
-        *kh = static_cast<int>(i % a.kv_heads);
-        const int64_t at = i / a.kv_heads;
+        const int64_t at = quotient(i, a.kv_heads);
+        *kh = static_cast<int>(i - at * a.kv_heads);
         int64_t run = 0;
         for (int b = 0; b < a.seqs; b += 32) {
             int start = 0, len = 0;
