@@ -12,6 +12,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 4096;
 
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const ServeArgs a, int64_t rows, bool singles_last, int capacity) {
+    allow_dependents();
     grid_dependency_wait();
     __shared__ int cursor[kPlanBuckets];
     __shared__ int sums[32];

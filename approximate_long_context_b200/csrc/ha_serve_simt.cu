@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const ServeArgs 
     extern __shared__ __align__(16) float sm[];
     __shared__ TreePiece piece;
     __shared__ int more;
+    allow_dependents();
     grid_dependency_wait();
     TreeWalk walk;
     const int warp = threadIdx.x >> 5, blocks = gridDim.x, block = blockIdx.x;
@@ -431,6 +432,7 @@ constexpr int kJoinRows = 4;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinRows) tree_join_kernel(const ServeArgs a, int blocks, int rows) {
+    allow_dependents();
     grid_dependency_wait();
     const TreeJoin j = tree_joins(a.ws)[blockIdx.x];
     const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;

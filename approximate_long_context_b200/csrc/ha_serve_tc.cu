@@ -338,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + C::kTmemSlot);
+    if (TREE || gridDim.x < a.sms) allow_dependents();
     grid_dependency_wait();   // what was in front on the stream, the list of prompt items among it
 
     // a wait of a whole warp: all of its lanes go on or none
