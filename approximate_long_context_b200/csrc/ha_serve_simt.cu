@@ -426,6 +426,258 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const ServeArgs 
     }
 }
 
+// ---- few rows: decoding and small trees over an fp32 cache
+//
+// At most 16 query rows, so reading the cache bounds it: tiles of 64 keys come with asynchronous copies, one ahead, and each
+// of the eight warps takes eight keys of a tile with a softmax of its own (no exchange between warps until the piece
+// ends). Scores: a lane has one row and two keys; product with V: a lane has d/32 columns of all rows.
+constexpr int kFewRows = 16, kWarps = kThreads / 32, kMine = kBN / kWarps;
+
+template <int D>
+struct Few {
+    static constexpr int LD = D + 4;
+    static constexpr int kQ = 0;
+    static constexpr int kKV = kFewRows * LD;              // two stages of K, then V
+    static constexpr int kTile = kBN * LD;
+    static constexpr int kP = kKV + 4 * kTile;             // [warp][key][row]
+    static constexpr int kStat = kP + kWarps * kMine * 20; // [warp][row] maximum, sum
+    static constexpr int kFloats = kStat + kWarps * kFewRows * 2;
+    static constexpr int kBytes = kFloats * 4;
+    static_assert(kWarps * kFewRows * D <= 4 * kTile, "the warps' numerators fit in the tiles' place");
+};
+
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool ok) {
+    const int n = ok ? 16 : 0;   // 0: zeros are written, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) tree_few_kernel(const ServeArgs a) {
+    using F = Few<D>;
+    constexpr int C = D / 32, kPer = kThreads / (D / 4), kTurns = kBN / kPer;
+    extern __shared__ __align__(16) float sm[];
+    __shared__ TreePiece piece;
+    __shared__ int more;
+    allow_dependents();
+    grid_dependency_wait();
+    TreeWalk walk;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, blocks = gridDim.x, block = blockIdx.x;
+    const int col = (tid % (D / 4)) * 4, row0 = tid / (D / 4);
+    const float c = a.scale * kLog2e;
+    float *Qs = sm + F::kQ, *Ps = sm + F::kP + warp * kMine * 20;
+    float2 *stat = reinterpret_cast<float2 *>(sm + F::kStat);
+    if (warp == 0) walk.begin(a, kBN, kBM, 0, block, blocks);
+    if (tid == 0) tree_joins(a.ws)[block].pieces = 0;
+    for (;;) {
+        __syncthreads();
+        if (warp == 0) {
+            TreePiece p;
+            const bool got = walk.next(a, kBN, kBM, 0, &p);
+            if (tid == 0) {
+                piece = p;
+                more = got;
+            }
+        }
+        __syncthreads();
+        if (!more) break;
+        const TreePiece w = piece;
+        const int rows = w.x.t * a.group, keys = w.x.len + w.x.t;
+        // pages of this thread's rows of a tile, and the copies of the tile into a stage
+        int ids[kTurns];
+        auto look = [&](int kt) {
+#pragma unroll
+            for (int u = 0; u < kTurns; ++u) {
+                const int key = kt * kBN + row0 + u * kPer;
+                ids[u] = kt < w.k1 && key < keys ? a.table[w.x.table + (key >> a.page_shift)] : -1;
+            }
+        };
+        auto copy = [&](int kt, int stage) {
+            float *Kd = sm + F::kKV + stage * 2 * F::kTile, *Vd = Kd + F::kTile;
+            if (kt < w.k1) {
+#pragma unroll
+                for (int u = 0; u < kTurns; ++u) {
+                    const int r = row0 + u * kPer, key = kt * kBN + r;
+                    const bool ok = key < keys && ids[u] >= 0 && ids[u] < a.pages;
+                    if (key < keys && !ok) atomicOr(a.status, kStatusData);
+                    const int64_t at = ok ? (((static_cast<int64_t>(ids[u]) * a.kv_heads + w.kh) << a.page_shift) +
+                                             (key & ((1 << a.page_shift) - 1))) * D + col
+                                          : 0;
+                    copy16(Kd + r * F::LD + col, static_cast<const float *>(a.kp) + at, ok);
+                    copy16(Vd + r * F::LD + col, static_cast<const float *>(a.vp) + at, ok);
+                }
+            }
+            cp_async_commit();
+        };
+        look(w.k0);
+        copy(w.k0, 0);
+        look(w.k0 + 1);
+        for (int x = tid; x < kFewRows * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), cc = (x % (D / 4)) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows) {
+                const int tok = r / a.group, head = w.kh * a.group + r - tok * a.group;
+                v = load4<float>(static_cast<const float *>(a.q) + static_cast<int64_t>(w.x.start + tok) * a.q_tok +
+                                 static_cast<int64_t>(head) * a.q_head + cc);
+            }
+            *reinterpret_cast<float4 *>(Qs + r * F::LD + cc) = v;
+        }
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[kFewRows][C];
+        uint64_t bits[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int r = g * 8 + (lane >> 2);
+            bits[g] = tree_bits(a, w.x.start, min(r, rows - 1) / a.group, w.x.t);
+        }
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r)
+#pragma unroll
+            for (int e = 0; e < C; ++e) acc[r][e] = 0.f;
+        const int groups = rows > 8 ? 2 : 1;
+        for (int kt = w.k0; kt < w.k1; ++kt) {
+            const int stage = (kt - w.k0) & 1;
+            copy(kt + 1, stage ^ 1);
+            look(kt + 2);
+            cp_async_wait<1>();
+            __syncthreads();   // the tile is there for all warps
+            const float *Ks = sm + F::kKV + stage * 2 * F::kTile + warp * kMine * F::LD, *Vs = Ks + F::kTile;
+            const int first = kt * kBN + warp * kMine;
+            const bool masked = first + kMine > w.x.len;
+            float alpha[2] = {1.f, 1.f};
+            if (first < keys) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (g >= groups) continue;
+                    const int r = g * 8 + (lane >> 2), k2 = (lane & 3) * 2;
+                    uint64_t s0 = 0, s1 = 0, t0 = 0, t1 = 0;
+#pragma unroll 8
+                    for (int d = 0; d < D; d += 4) {
+                        const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(Qs + r * F::LD + d);
+                        const ulonglong2 ka = *reinterpret_cast<const ulonglong2 *>(Ks + k2 * F::LD + d);
+                        const ulonglong2 kb = *reinterpret_cast<const ulonglong2 *>(Ks + (k2 + 1) * F::LD + d);
+                        s0 = f2_fma(q.x, ka.x, s0);
+                        t0 = f2_fma(q.y, ka.y, t0);
+                        s1 = f2_fma(q.x, kb.x, s1);
+                        t1 = f2_fma(q.y, kb.y, t1);
+                    }
+                    const float2 u0 = f2_unpack(f2_add(s0, t0)), u1 = f2_unpack(f2_add(s1, t1));
+                    float x0 = (u0.x + u0.y) * c, x1 = (u1.x + u1.y) * c;
+                    const int key = first + k2;
+                    const bool see0 = key < w.x.len || (key < keys && (bits[g] >> (key - w.x.len) & 1));
+                    const bool see1 = key + 1 < w.x.len || (key + 1 < keys && (bits[g] >> (key + 1 - w.x.len) & 1));
+                    float top = fmaxf(see0 ? x0 : -INFINITY, see1 ? x1 : -INFINITY);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const float mn = fmaxf(m[g], top), ref = mn == -INFINITY ? 0.f : mn;
+                    alpha[g] = exp2f(m[g] - ref);
+                    m[g] = mn;
+                    x0 = see0 ? exp2f(x0 - ref) : 0.f;
+                    x1 = see1 ? exp2f(x1 - ref) : 0.f;
+                    l[g] = l[g] * alpha[g] + x0 + x1;
+                    Ps[k2 * 20 + r] = x0;
+                    Ps[(k2 + 1) * 20 + r] = x1;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (g >= groups) continue;
+                    if (__any_sync(0xffffffffu, alpha[g] != 1.f)) {
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const float f = __shfl_sync(0xffffffffu, alpha[g], r * 4);
+#pragma unroll
+                            for (int e = 0; e < C; ++e) acc[g * 8 + r][e] *= f;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < kMine; ++k) {
+                        float v[C];
+                        if (C == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(Vs + k * F::LD + lane * 4);
+                        else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(Vs + k * F::LD + lane * 2);
+                        const float4 pa = *reinterpret_cast<const float4 *>(Ps + k * 20 + g * 8);
+                        const float4 pb = *reinterpret_cast<const float4 *>(Ps + k * 20 + g * 8 + 4);
+                        const float p[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+#pragma unroll
+                            for (int e = 0; e < C; ++e)   // a masked key's value may be no number
+                                if (!masked || p[r] != 0.f) acc[g * 8 + r][e] = fmaf(p[r], v[e], acc[g * 8 + r][e]);
+                    }
+                }
+            }
+            __syncthreads();   // the stage may be filled again
+        }
+        // ---- the warps' results joined: numerators to the tiles' place, then one sum per row and column
+        float *part = sm + F::kKV;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            l[g] += __shfl_xor_sync(0xffffffffu, l[g], 1);
+            l[g] += __shfl_xor_sync(0xffffffffu, l[g], 2);
+            if ((lane & 3) == 0) stat[warp * kFewRows + g * 8 + (lane >> 2)] = make_float2(m[g], l[g]);
+        }
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r)
+            if (r < rows) {
+                if (C == 4) *reinterpret_cast<float4 *>(part + (warp * kFewRows + r) * D + lane * 4) = *reinterpret_cast<float4 *>(acc[r]);
+                else *reinterpret_cast<float2 *>(part + (warp * kFewRows + r) * D + lane * 2) = *reinterpret_cast<float2 *>(acc[r]);
+            }
+        __syncthreads();
+        const bool whole = w.k0 == 0 && w.k1 == w.nk;
+        float *slot = whole ? nullptr : tree_slot(a.ws, blocks, 2 * block + (w.k0 == 0), kFewRows, D);
+        for (int x = tid; x < rows * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), cc = (x % (D / 4)) * 4;
+            float mt = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) mt = fmaxf(mt, stat[i * kFewRows + r].x);
+            const float ref = mt == -INFINITY ? 0.f : mt;
+            float lt = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float2 st = stat[i * kFewRows + r];
+                const float f = exp2f(st.x - ref);
+                const float4 v = *reinterpret_cast<const float4 *>(part + (i * kFewRows + r) * D + cc);
+                lt = fmaf(f, st.y, lt);
+                o[0] = fmaf(f, v.x, o[0]);
+                o[1] = fmaf(f, v.y, o[1]);
+                o[2] = fmaf(f, v.z, o[2]);
+                o[3] = fmaf(f, v.w, o[3]);
+            }
+            if (slot) {
+                *reinterpret_cast<float4 *>(slot + r * D + cc) = make_float4(o[0], o[1], o[2], o[3]);
+                if (cc == 0) {
+                    slot[kFewRows * D + r] = mt;
+                    slot[kFewRows * (D + 1) + r] = lt;
+                }
+                continue;
+            }
+            const int tok = r / a.group, head = w.kh * a.group + r - tok * a.group;
+            const int64_t at = static_cast<int64_t>(w.x.start + tok) * a.o_tok + static_cast<int64_t>(head) * a.o_head + cc;
+            const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = lt == 0.f ? 0.f : o[e] * inv;
+            if (a.out_dtype == 0) {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
+                uint2 u;
+                u.x = *reinterpret_cast<const uint32_t *>(&lo);
+                u.y = *reinterpret_cast<const uint32_t *>(&hi);
+                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + at) = u;
+            } else {
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at) = make_float4(o[0], o[1], o[2], o[3]);
+            }
+            if (a.lse && cc == 0)
+                a.lse[static_cast<int64_t>(head) * a.tokens + w.x.start + tok] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
+        }
+        if (w.k0 == 0 && !whole && tid == 0) {
+            TreeJoin j{};
+            j.pieces = tree_pieces(w, block);
+            j.start = w.x.start;
+            j.row0 = 0;
+            j.rows = rows;
+            j.kh = w.kh;
+            tree_joins(a.ws)[block] = j;
+        }
+    }
+}
+
 // Joins the pieces of the segment that block blockIdx.x begins and does not end: one warp per row, the pieces' numerators
 // and sums weighted with 2^(m_piece - m). The order is fixed, so equal calls give equal bits.
 constexpr int kJoinRows = 4;
@@ -513,6 +765,15 @@ int prompt_simt(const ServeArgs &a, cudaStream_t st) {
     return launch_dependent(prompt_simt_kernel<D, T>, grid, dim3(kThreads), Smem<D>::kBytes, st, a, listed) ? 1 + listed : -1;
 }
 
+template <int D>
+int tree_few(const ServeArgs &a, cudaStream_t st) {
+    static std::atomic<uint64_t> known{0};
+    if (!allow_smem(tree_few_kernel<D>, Few<D>::kBytes, &known)) return -1;
+    const int blocks = a.sms * (D == 64 ? 2 : 1);   // by shared memory
+    if (!launch_dependent(tree_few_kernel<D>, dim3(blocks), dim3(kThreads), Few<D>::kBytes, st, a)) return -1;
+    return launch_tree_join(a, blocks, kFewRows, st) ? 2 : -1;
+}
+
 template <int D, typename T>
 int tree_simt(const ServeArgs &a, cudaStream_t st) {
     static std::atomic<uint64_t> known{0};
@@ -549,8 +810,9 @@ int launch_prompt_simt(const ServeArgs &a, int dtype, cudaStream_t st) {
 }
 
 int launch_tree_simt(const ServeArgs &a, int dtype, cudaStream_t st) {
-    if (a.d == 64) return dtype == 0 ? tree_simt<64, uint16_t>(a, st) : tree_simt<64, float>(a, st);
-    return dtype == 0 ? tree_simt<128, uint16_t>(a, st) : tree_simt<128, float>(a, st);
+    const bool few = dtype != 0 && a.max_len * a.group <= kFewRows;
+    if (a.d == 64) return few ? tree_few<64>(a, st) : dtype == 0 ? tree_simt<64, uint16_t>(a, st) : tree_simt<64, float>(a, st);
+    return few ? tree_few<128>(a, st) : dtype == 0 ? tree_simt<128, uint16_t>(a, st) : tree_simt<128, float>(a, st);
 }
 
 }  // namespace ha
