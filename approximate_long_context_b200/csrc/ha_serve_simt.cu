@@ -44,14 +44,22 @@ __device__ __forceinline__ bool finite4(float4 v) {
     return fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY && fabsf(v.w) < INFINITY;
 }
 
-template <int D>
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool ok) {
+    const int n = ok ? 16 : 0;   // 0: zeros are written, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+
+template <int D, typename T>
 struct Smem {
+    // fp32 at d = 64: the next tile comes with asynchronous copies while one is worked on, with two blocks per SM still
+    static constexpr bool kAsync = D == 64 && sizeof(T) == 4;
     static constexpr int LD = D + 4;      // row pitch: 16-byte aligned, eight consecutive rows on different banks
     static constexpr int LP = kBN + 4;
     static constexpr int kQ = 0;
     static constexpr int kK = kBM * LD;   // P overwrites K once the scores are done
     static constexpr int kV = kK + kBN * LD;
-    static constexpr int kFloats = kV + kBN * LD;
+    static constexpr int kStage = 2 * kBN * LD;   // K and V of a tile
+    static constexpr int kFloats = kK + (kAsync ? 2 : 1) * kStage;
     static constexpr int kBytes = kFloats * 4;
     static_assert(kBM * LP <= kBN * LD, "P fits in K's place");
 };
@@ -67,9 +75,9 @@ struct Work {
 template <int D, bool TREE, typename T>
 __device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float *sm, float (&acc)[4][D / 16], float (&m)[4],
                                        float (&l)[4]) {
-    using S = Smem<D>;
+    using S = Smem<D, T>;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    float *Qs = sm + S::kQ, *Ks = sm + S::kK, *Ps = Ks, *Vs = sm + S::kV;
+    float *Qs = sm + S::kQ, *Ks = sm + S::kK, *Vs = sm + S::kV;
     const float c = a.scale * kLog2e;
     const T *q = static_cast<const T *>(a.q);
     const bool busy = (tid >> 5) * 8 < w.rows;   // some row of the warp
@@ -101,54 +109,81 @@ __device__ __forceinline__ void attend(const ServeArgs &a, const Work &w, float 
     const int keys = w.len + w.t;
     // the first key that some row of the tile does not see
     const int masked_from = TREE ? w.len : w.row0 / a.group + 1;
-    for (int kt = w.k0; kt < w.k1; ++kt) {
-        const int base = kt * kBN;
-        __syncthreads();   // the previous tile's P and V have been read
-        bool odd = false;
-        // four rows' pieces of K and V in flight per thread (one after the other, a tile took eight memory latencies)
-        constexpr int kPer = kThreads / (D / 4), kBatch = 4;   // rows per turn of the block
-        const int col = (tid % (D / 4)) * 4;
-        for (int r0 = tid / (D / 4); r0 < kBN; r0 += kPer * kBatch) {
-            float4 kv[kBatch], vv[kBatch];
-            int64_t ko[kBatch], vo[kBatch];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int key = base + r0 + u * kPer;
-                ko[u] = vo[u] = -1;
-                if (key < keys) {
-                    if (TREE) {
-                        const int32_t page = a.table[w.table + (key >> a.page_shift)];
-                        if (page >= 0 && page < a.pages) {
-                            ko[u] = vo[u] = (((static_cast<int64_t>(page) * a.kv_heads + w.kh) << a.page_shift) +
-                                             (key & ((1 << a.page_shift) - 1))) * D + col;
-                        } else {
-                            atomicOr(a.status, kStatusData);
-                        }
-                    } else {
-                        const int64_t row = w.start + key;
-                        ko[u] = row * a.k_tok + w.kh * a.k_head + col;
-                        vo[u] = row * a.v_tok + w.kh * a.v_head + col;
-                    }
-                }
+    constexpr int kPer = kThreads / (D / 4);   // rows per turn of the block
+    const int col = (tid % (D / 4)) * 4;
+    // where this thread's piece of a key's K and V rows lies; false: zeros
+    auto place = [&](int key, int64_t *ko, int64_t *vo) -> bool {
+        if (key >= keys) return false;
+        if (TREE) {
+            const int32_t page = a.table[w.table + (key >> a.page_shift)];
+            if (page < 0 || page >= a.pages) {
+                atomicOr(a.status, kStatusData);
+                return false;
             }
+            *ko = *vo = (((static_cast<int64_t>(page) * a.kv_heads + w.kh) << a.page_shift) +
+                         (key & ((1 << a.page_shift) - 1))) * D + col;
+        } else {
+            const int64_t row = w.start + key;
+            *ko = row * a.k_tok + w.kh * a.k_head + col;
+            *vo = row * a.v_tok + w.kh * a.v_head + col;
+        }
+        return true;
+    };
+    const T *kp = static_cast<const T *>(TREE ? a.kp : a.k), *vp = static_cast<const T *>(TREE ? a.vp : a.v);
+    auto copy = [&](int kt, int stage) {   // kAsync
+        if (kt < w.k1) {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                kv[u] = vv[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (ko[u] >= 0) {
-                    kv[u] = load4<T>(static_cast<const T *>(TREE ? a.kp : a.k) + ko[u]);
-                    vv[u] = load4<T>(static_cast<const T *>(TREE ? a.vp : a.v) + vo[u]);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int r = r0 + u * kPer;
-                odd |= !finite4(vv[u]);
-                *reinterpret_cast<float4 *>(Ks + r * S::LD + col) = kv[u];
-                *reinterpret_cast<float4 *>(Vs + r * S::LD + col) = vv[u];
+            for (int r = tid / (D / 4); r < kBN; r += kPer) {
+                int64_t ko = 0, vo = 0;
+                const bool ok = place(kt * kBN + r, &ko, &vo);
+                float *to = sm + S::kK + stage * S::kStage + r * S::LD + col;
+                copy16(to, reinterpret_cast<const float *>(kp) + ko, ok);
+                copy16(to + kBN * S::LD, reinterpret_cast<const float *>(vp) + vo, ok);
             }
         }
+        cp_async_commit();
+    };
+    if (S::kAsync) copy(w.k0, 0);
+    for (int kt = w.k0; kt < w.k1; ++kt) {
+        const int base = kt * kBN;
+        bool odd = false;
+        if (S::kAsync) {
+            Ks = sm + S::kK + ((kt - w.k0) & 1) * S::kStage;
+            Vs = Ks + kBN * S::LD;
+            cp_async_wait<0>();
+#pragma unroll
+            for (int r = tid / (D / 4); r < kBN; r += kPer) odd |= !finite4(*reinterpret_cast<const float4 *>(Vs + r * S::LD + col));
+        } else {
+            __syncthreads();   // the previous tile's P and V have been read
+            // some rows' pieces of K and V in flight per thread (one after the other, a tile took eight memory latencies)
+            constexpr int kBatch = D == 64 ? 4 : 2;
+            for (int r0 = tid / (D / 4); r0 < kBN; r0 += kPer * kBatch) {
+                float4 kv[kBatch], vv[kBatch];
+                int64_t ko[kBatch], vo[kBatch];
+                bool ok[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) ok[u] = place(base + r0 + u * kPer, &ko[u], &vo[u]);
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    kv[u] = vv[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (ok[u]) {
+                        kv[u] = load4<T>(kp + ko[u]);
+                        vv[u] = load4<T>(vp + vo[u]);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int r = r0 + u * kPer;
+                    odd |= !finite4(vv[u]);
+                    *reinterpret_cast<float4 *>(Ks + r * S::LD + col) = kv[u];
+                    *reinterpret_cast<float4 *>(Vs + r * S::LD + col) = vv[u];
+                }
+            }
+        }
+        float *Ps = Ks;
         const bool masked = base + kBN > masked_from || base + kBN > keys;
         const bool select = __syncthreads_or(odd) && masked;
+        if (S::kAsync) copy(kt + 1, (kt + 1 - w.k0) & 1);   // the other stage's P and V have been read
         // two partial sums per score, over the even and the odd of the d products, in packed instructions
         uint64_t s2[4][4];
 #pragma unroll
@@ -445,11 +480,6 @@ struct Few {
     static constexpr int kBytes = kFloats * 4;
     static_assert(kWarps * kFewRows * D <= 4 * kTile, "the warps' numerators fit in the tiles' place");
 };
-
-__device__ __forceinline__ void copy16(float *dst, const float *src, bool ok) {
-    const int n = ok ? 16 : 0;   // 0: zeros are written, nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) tree_few_kernel(const ServeArgs a) {
@@ -755,14 +785,14 @@ __global__ void __launch_bounds__(32 * kJoinRows) tree_join_kernel(const ServeAr
 template <int D, typename T>
 int prompt_simt(const ServeArgs &a, cudaStream_t st) {
     static std::atomic<uint64_t> known{0};
-    if (!allow_smem(prompt_simt_kernel<D, T>, Smem<D>::kBytes, &known)) return -1;
+    if (!allow_smem(prompt_simt_kernel<D, T>, Smem<D, T>::kBytes, &known)) return -1;
     const int64_t tiles = prompt_items(a.tokens, a.seqs, kBM, a.group);
     // blocks of a grid; row numbers within a sequence
     if (tiles * a.kv_heads > 0x7fffffff || static_cast<int64_t>(a.max_len) * a.group > 0x7fffff00) return -2;
     const bool listed = a.seqs > 32;
     if (listed && !launch_prompt_plan(a, kBM, false, tiles, st)) return -1;
     const dim3 grid(static_cast<unsigned>(tiles * a.kv_heads));
-    return launch_dependent(prompt_simt_kernel<D, T>, grid, dim3(kThreads), Smem<D>::kBytes, st, a, listed) ? 1 + listed : -1;
+    return launch_dependent(prompt_simt_kernel<D, T>, grid, dim3(kThreads), Smem<D, T>::kBytes, st, a, listed) ? 1 + listed : -1;
 }
 
 template <int D>
@@ -777,9 +807,9 @@ int tree_few(const ServeArgs &a, cudaStream_t st) {
 template <int D, typename T>
 int tree_simt(const ServeArgs &a, cudaStream_t st) {
     static std::atomic<uint64_t> known{0};
-    if (!allow_smem(tree_simt_kernel<D, T>, Smem<D>::kBytes, &known)) return -1;
+    if (!allow_smem(tree_simt_kernel<D, T>, Smem<D, T>::kBytes, &known)) return -1;
     const int blocks = 2 * a.sms;   // two per SM fit (shared memory)
-    if (!launch_dependent(tree_simt_kernel<D, T>, dim3(blocks), dim3(kThreads), Smem<D>::kBytes, st, a)) return -1;
+    if (!launch_dependent(tree_simt_kernel<D, T>, dim3(blocks), dim3(kThreads), Smem<D, T>::kBytes, st, a)) return -1;
     return launch_tree_join(a, blocks, kBM, st) ? 2 : -1;
 }
 
