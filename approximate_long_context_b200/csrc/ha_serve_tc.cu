@@ -325,6 +325,17 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
         *abort_flag = 0;
         fence_mbar_init();
     }
+    // Rows of the Q tiles that no load brings are zeros, so that their scores, weights and products are: multiplying what
+    // happened to lie there draws power, and the clock gives way to power (64 users decoding, sustained: 365 -> 331 us).
+    if (x.box_rows < 128) {
+        const int rows = 128 - x.box_rows;
+        for (int e = threadIdx.x; e < C::NQ * (D / 64) * rows * 8; e += kThreads) {
+            const int part = e / (rows * 8), y = e - part * rows * 8;
+            *reinterpret_cast<uint4 *>(sm + C::kQ + part * 16384 + (x.box_rows + (y >> 3)) * 128 + (y & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+    }
     if (warp == 0) {
         if (lane == 0) {
             prefetch_map(&maps.q);
