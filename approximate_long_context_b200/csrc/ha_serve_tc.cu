@@ -7,6 +7,11 @@
 //   PAIR: two neighbouring query tiles over the same key tiles (prompts; drafts of more than one tile);
 //   ALT:  one query tile, tile t takes every other key tile; the two results are joined in the epilogue (decoding and
 //         small trees, which are bound by reading the cache).
+//   ALT16: ALT for d = 128 and pages of 16 rows. A load of a page brings one box of 64 columns; with 2 KB boxes the copy
+//         engine and not the memory is the bound (64 users decoding: 424 us, against 330 us with larger pages and 342 us
+//         here; 16 trees of 32 tokens: 100 -> 83 us). Here a box has both halves of the page's rows (4 KB). A key tile then lies page by page, [half][16 rows][128 bytes], which
+//         the score product reads as two products of 64 keys, rows 0-7 and rows 8-15 of the eight pages; the softmax
+//         puts the keys back in order when it writes P.
 // Tree items come from an even cut of all key tiles over the blocks (TreeWalk); pieces of a cut segment go to the
 // workspace and a second kernel joins them.
 //
@@ -52,7 +57,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.0f;
 
-enum { PROMPT = 0, TREE_PAIR = 1, TREE_ALT = 2 };
+enum { PROMPT = 0, TREE_PAIR = 1, TREE_ALT = 2, TREE_ALT16 = 3 };
 
 // One work item, published by the loader.
 struct Item {
@@ -72,7 +77,7 @@ constexpr int kItems = 4;
 
 template <int D, int MODE>
 struct Cfg {
-    static constexpr bool ALT = MODE == TREE_ALT;
+    static constexpr bool ALT = MODE == TREE_ALT || MODE == TREE_ALT16, P16 = MODE == TREE_ALT16;
     static constexpr int kTile = 128 * D * 2;      // 128 rows of bf16
     static constexpr int NQ = ALT ? 1 : 2;
     static constexpr int NK = D == 64 ? (ALT ? 6 : 5) : (ALT ? 3 : 2);
@@ -133,6 +138,11 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, uin
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w) {
     asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::
                      "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w, int v) {
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::
+                     "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
                  : "memory");
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
@@ -282,7 +292,7 @@ __device__ __forceinline__ bool elect_one() {
 template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, const __grid_constant__ Maps maps) {
     using C = Cfg<D, MODE>;
-    constexpr bool ALT = C::ALT, TREE = MODE != PROMPT;
+    constexpr bool ALT = C::ALT, TREE = MODE != PROMPT, P16 = C::P16;
     const ServeArgs &a = x.a;
     extern __shared__ __align__(1024) unsigned char sm[];   // the swizzled tiles need the alignment; there is no room to pad
     const uint32_t sbase = smem_addr(sm);
@@ -462,9 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                     if (lane < per_tile) {
                         const int z = id < 0 ? static_cast<int>(a.pages) : id;   // past the last page: zeros
                         const int y = page > 128 ? (kt * 128) & (page - 1) : 0;
+                        if (P16) {
+                            tma_5d(dst + lane * 4096, map, b, 0, 0, 0, kh, z);
+                        } else {
 #pragma unroll
-                        for (int h = 0; h < D / 64; ++h)
-                            tma_4d(dst + h * 16384 + lane * (page << 7), map, b, h * 64, y, kh, z);
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_4d(dst + h * 16384 + lane * (page << 7), map, b, h * 64, y, kh, z);
+                        }
                     }
                 } else if (lane == 0) {
 #pragma unroll
@@ -528,11 +542,11 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
         // scheduler's instruction cache with two softmax warps, and a straight-line version spent about 200 cycles per
         // wait on fetching itself.
         const bool leader = elect_one();
-        constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false, false);
+        constexpr uint32_t idesc_qk = idesc_bf16(128, P16 ? 64 : 128, false, false);
         constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
         const uint64_t dq0 = smem_desc(sbase + C::kQ, 16, 1024);
-        const uint64_t dk0 = smem_desc(sbase + C::kK, 16, 1024);
-        const uint64_t dv0 = smem_desc(sbase + C::kV, 16384, 1024);
+        const uint64_t dk0 = smem_desc(sbase + C::kK, 16, P16 ? 4096 : 1024);
+        const uint64_t dv0 = smem_desc(sbase + C::kV, P16 ? 2048 : 16384, 1024);
         bool ok = true;
         uint32_t base = 0, idx = 0;          // number of the item's first key tile among the block's loads; the item
         uint32_t cq = 0, cp = 0, co = 0;     // parities, bit t: Q tiles waited for (ALT: bit 0), P tiles consumed, items begun
@@ -582,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                         if (leader) {
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
-                                mma_ts(tO, tP + kk * 8, dv + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
+                                mma_ts(tO, tP + kk * 8, dv + static_cast<uint64_t>((kk * (P16 ? 4096 : 2048)) >> 4), idesc_pv,
                                        (j > 0 || kk > 0) ? 1u : 0u);
                             if (two || t == 1 || j >= n1) mma_commit(bar(C::bVEmpty + vs));
                             if (j == n - 1) mma_commit(bar(C::bODone + t));
@@ -617,7 +631,13 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-                            mma_ss(tS, dq + off, dk + off, idesc_qk, kk > 0 ? 1u : 0u);
+                            if (P16) {
+                                const uint64_t offk = static_cast<uint64_t>(((kk >> 2) * 2048 + (kk & 3) * 32) >> 4);
+                                mma_ss(tS, dq + off, dk + offk, idesc_qk, kk > 0 ? 1u : 0u);
+                                mma_ss(tS + 64, dq + off, dk + offk + (1024 >> 4), idesc_qk, kk > 0 ? 1u : 0u);
+                            } else {
+                                mma_ss(tS, dq + off, dk + off, idesc_qk, kk > 0 ? 1u : 0u);
+                            }
                         }
                         mma_commit(bar(C::bSFull + t));
                         if (turns || t == 1 || k >= e1) mma_commit(bar(C::bKEmpty + ks));
@@ -798,8 +818,23 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                         // Diagonal tiles, and ALT, which waits for memory: 32 scores at a time, twice, without the quarters that
                         // no row sees (256 short prompts: 88 -> 69 us)
                         auto read = [&](int h, uint32_t (&s)[32]) {
-                            tmem_ld32(tS + h * 32, s);
-                            tmem_ld_wait();
+                            if (P16) {
+                                // rows 0-7 and rows 8-15 of two pages, put in the keys' order
+                                uint32_t lo[16], hi[16];
+                                tmem_ld16(tS + h * 16, lo);
+                                tmem_ld16(tS + 64 + h * 16, hi);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    s[e] = lo[e];
+                                    s[8 + e] = hi[e];
+                                    s[16 + e] = lo[8 + e];
+                                    s[24 + e] = hi[8 + e];
+                                }
+                            } else {
+                                tmem_ld32(tS + h * 32, s);
+                                tmem_ld_wait();
+                            }
                             if (kt >= masked) {
                                 const uint32_t w = seen_of(h);
                                 if (!__all_sync(0xffffffffu, w == 0xffffffffu)) conceal(w, s);
@@ -1144,15 +1179,21 @@ int launch_tree_tc(const ServeArgs &a, cudaStream_t st) {
     x.box_rows = box_tokens * a.group;
     const bool alt = a.max_len <= x.tpt;
     const int page = 1 << a.page_shift;
+    const bool p16 = alt && a.d == 128 && page == 16;
     Maps maps;
     const int64_t dims[4] = {a.d, page, a.kv_heads, a.pages};
     const int64_t strides[3] = {a.d, static_cast<int64_t>(a.d) * page, static_cast<int64_t>(a.d) * page * a.kv_heads};
     const int box[4] = {64, page < 128 ? page : 128, 1, 1};
+    const int64_t dims16[5] = {64, 16, 2, a.kv_heads, a.pages};
+    const int64_t strides16[4] = {128, 64, 128 * 16, static_cast<int64_t>(128) * 16 * a.kv_heads};
+    const int box16[5] = {64, 16, 2, 1, 1};
     if (!make_rows_map(&maps.q, a.q, a.d, a.heads, a.tokens, a.q_head, a.q_tok, a.group, box_tokens) ||
-        !make_map(&maps.k, a.kp, 4, dims, strides, box) || !make_map(&maps.v, a.vp, 4, dims, strides, box))
+        !(p16 ? make_map(&maps.k, a.kp, 5, dims16, strides16, box16) : make_map(&maps.k, a.kp, 4, dims, strides, box)) ||
+        !(p16 ? make_map(&maps.v, a.vp, 5, dims16, strides16, box16) : make_map(&maps.v, a.vp, 4, dims, strides, box)))
         return -2;
     bool ok;
-    if (alt) ok = a.d == 64 ? launch<64, TREE_ALT>(x, maps, a.sms, st) : launch<128, TREE_ALT>(x, maps, a.sms, st);
+    if (p16) ok = launch<128, TREE_ALT16>(x, maps, a.sms, st);
+    else if (alt) ok = a.d == 64 ? launch<64, TREE_ALT>(x, maps, a.sms, st) : launch<128, TREE_ALT>(x, maps, a.sms, st);
     else ok = a.d == 64 ? launch<64, TREE_PAIR>(x, maps, a.sms, st) : launch<128, TREE_PAIR>(x, maps, a.sms, st);
     if (!ok) return -1;
     return launch_tree_join(a, a.sms, alt ? 128 : 256, st) ? 2 : -1;
