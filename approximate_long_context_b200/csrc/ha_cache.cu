@@ -330,10 +330,18 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const ServeCache c, i
     const int64_t t = blockIdx.x;
     // the sequence that holds token t: the last one whose offset is not behind it
     int lo = 0, hi = n;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid + 1] > t) hi = mid;
-        else lo = mid + 1;
+    const bool few = n <= 256;   // an entry per thread: two loads in a row instead of one for each halving
+    int32_t slot = 0;
+    if (few) {
+        const bool mine = threadIdx.x < n;
+        slot = mine ? slots[threadIdx.x] : 0;
+        lo = __syncthreads_count(mine && cu[threadIdx.x + 1] <= t);
+    } else {
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (cu[mid + 1] > t) hi = mid;
+            else lo = mid + 1;
+        }
     }
     if (lo >= n) return;   // behind the last sequence
     const int64_t start = cu[lo];
@@ -348,9 +356,11 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const ServeCache c, i
     }
     const int64_t len = c.lens[s], at = len + t - start, pi = at >> c.page_shift;
     const int held = c.held[s];
+    // two entries of a slot would write the same rows
+    const bool dup = few ? __syncthreads_or(threadIdx.x < lo && slot == s) : block_contains(slots, lo, s);
     int32_t id = -1;
     if (len >= 0 && pi < held && held <= c.max_pages) id = c.table[s * c.max_pages + pi];
-    if (id < 0 || id >= c.pages || c.refs[id] != 1) {   // a page that another slot shares is not written
+    if (dup || id < 0 || id >= c.pages || c.refs[id] != 1) {   // a page that another slot shares is not written
         if (threadIdx.x == 0) atomicOr(status, kStatusData);
         return;
     }
@@ -401,22 +411,26 @@ __device__ bool commit_entry(const ServeCache &c, const int32_t *slots, const in
             bad |= x < 0 || x >= room || (j > 0 && x <= mine[j - 1]);
         }
     }
-    // the pages that rows are read from and written to
+    // the pages that rows are read from and written to; none that another slot shares is written
     const int32_t *row = c.table + s * c.max_pages;
-    for (int p = (*len >> c.page_shift) + threadIdx.x; p < *held; p += blockDim.x) bad |= row[p] < 0 || row[p] >= c.pages;
+    const int written = keep && *count > 0 ? (*len + *count + c.page - 1) >> c.page_shift : 0;
+    for (int p = (*len >> c.page_shift) + threadIdx.x; p < *held; p += blockDim.x) {
+        const int32_t id = row[p];
+        const bool out = id < 0 || id >= c.pages;
+        bad |= out || (p < written && c.refs[id] != 1);
+    }
     return !__syncthreads_or(bad);
 }
 
 constexpr int kMoveChunk = 256;   // kept rows staged at a time
 
-// The kept rows of a draft move to the front of it, in one layer of k or v: row len + keep[i] -> len + i. keep is ascending,
+// The kept rows of a draft move to the front of it, in one layer of k and v: row len + keep[i] -> len + i. keep is ascending,
 // so keep[i] >= i and a row is read before a later row is written over it; every thread moves its own 16-byte column in
 // ascending order, eight rows in flight.
-__device__ __forceinline__ void move_rows(const ServeCache &c, int esz, char *base, int64_t layer, const int32_t *row, int len,
+__device__ __forceinline__ void move_rows(const ServeCache &c, int esz, int64_t layer, const int32_t *row, int len,
                                           const int32_t *mine, int count, int64_t *from, int64_t *to) {
     const int64_t row_bytes = static_cast<int64_t>(c.d) * esz, head_bytes = row_bytes * c.page,
                   page_bytes = head_bytes * c.kv_heads;
-    base += layer * c.pages * page_bytes;
     const int per_row = static_cast<int>(row_bytes / 16), total = per_row * c.kv_heads;
     for (int first = 0; first < count; first += kMoveChunk) {
         const int m = min(kMoveChunk, count - first);
@@ -427,8 +441,10 @@ __device__ __forceinline__ void move_rows(const ServeCache &c, int esz, char *ba
             to[j] = row[b >> c.page_shift] * page_bytes + (b & (c.page - 1)) * row_bytes;
         }
         __syncthreads();
-        for (int x = threadIdx.x; x < total; x += blockDim.x) {
-            char *col = base + (x / per_row) * head_bytes + (x % per_row) * 16;
+        for (int y = threadIdx.x; y < 2 * total; y += blockDim.x) {
+            const int x = y < total ? y : y - total;
+            char *col = static_cast<char *>(y < total ? c.k : c.v) + layer * c.pages * page_bytes + (x / per_row) * head_bytes +
+                        (x % per_row) * 16;
             for (int j0 = 0; j0 < m; j0 += 8) {
                 int4 buf[8];
 #pragma unroll
@@ -442,7 +458,7 @@ __device__ __forceinline__ void move_rows(const ServeCache &c, int esz, char *ba
     }
 }
 
-// One block per (entry, layer, k or v).
+// One block per (entry, layer).
 __global__ void __launch_bounds__(128) cache_commit_move_kernel(const ServeCache c, int esz, const int32_t *slots,
                                                                 const int32_t *counts, const int32_t *keep,
                                                                 int64_t max_keep) {
@@ -450,8 +466,7 @@ __global__ void __launch_bounds__(128) cache_commit_move_kernel(const ServeCache
     __shared__ int64_t from[kMoveChunk], to[kMoveChunk];   // byte offsets of the rows in a layer, head 0
     int len = 0, held = 0, count = 0;
     if (!commit_entry(c, slots, counts, keep, max_keep, blockIdx.x, &len, &held, &count)) return;   // flagged below
-    move_rows(c, esz, static_cast<char *>((blockIdx.y & 1) ? c.v : c.k), blockIdx.y >> 1,
-              c.table + static_cast<int64_t>(slots[blockIdx.x]) * c.max_pages, len,
+    move_rows(c, esz, blockIdx.y, c.table + static_cast<int64_t>(slots[blockIdx.x]) * c.max_pages, len,
               keep + static_cast<int64_t>(blockIdx.x) * max_keep, count, from, to);
 }
 
@@ -469,9 +484,8 @@ __global__ void __launch_bounds__(128) cache_commit_kernel(const ServeCache c, i
     const int32_t s = slots[blockIdx.x];
     int32_t *row = c.table + static_cast<int64_t>(s) * c.max_pages;
     if (move) {
-        for (int y = 0; y < 2 * static_cast<int>(c.layers); ++y)
-            move_rows(c, esz, static_cast<char *>((y & 1) ? c.v : c.k), y >> 1, row, len,
-                      keep + static_cast<int64_t>(blockIdx.x) * max_keep, count, from, to);
+        for (int y = 0; y < static_cast<int>(c.layers); ++y)
+            move_rows(c, esz, y, row, len, keep + static_cast<int64_t>(blockIdx.x) * max_keep, count, from, to);
         __syncthreads();   // the table has been read
     }
     const int after = (len + count + c.page - 1) >> c.page_shift;
@@ -537,7 +551,7 @@ int launch_cache_commit(const ServeCache &c, int esz, const int32_t *slots, cons
     const bool move = keep && row_bytes_all(c, esz) <= 16 * 1024;
     int launches = 0;
     if (keep && !move) {
-        const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(2 * c.layers));
+        const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(c.layers));
         if (!launch_dependent(cache_commit_move_kernel, grid, dim3(128), 0, st, c, esz, slots, counts, keep, max_keep)) return -1;
         ++launches;
     }

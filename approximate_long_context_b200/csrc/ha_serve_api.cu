@@ -281,7 +281,7 @@ int hyper_attn_cache_append(hyper_attn_t h, const ha_cache *cache, const int32_t
     return guarded(h, [&]() -> int {
         ha::ServeCache c;
         int rc = check_cache(h, cache, &c);
-        if (rc || (rc = check_count(h, n, 1 << 20))) return rc;
+        if (rc || (rc = check_count(h, n, 65536))) return rc;
         if (tokens < 0 || tokens > kMaxTokens) return fail(h, HA_ERR_INVALID_ARG, "tokens must lie in [0, 2^30]");
         if (layer < 0 || layers < 1 || layer > c.layers - layers) return fail(h, HA_ERR_INVALID_ARG, "layers out of range");
         h->last_launches = 0;

@@ -376,8 +376,9 @@ typedef struct {
 HA_API size_t hyper_attn_tree_workspace(hyper_attn_t h, int d);
 HA_API int hyper_attn_tree(hyper_attn_t h, const ha_cache *cache, const ha_tree_args *args);
 
-/* The cache's steps; n entries (n = 0: nothing is done; at most 16384, append 2^20), all lists in device memory. A slot named twice in one
- * call counts once (the first time) and is reported by hyper_attn_status like an entry out of range.
+/* The cache's steps; n entries (n = 0: nothing is done; at most 16384, append 65536), all lists in device memory. A
+ * slot named twice in one call counts once (the first time) and is reported by hyper_attn_status like an entry out of
+ * range.
  *   free     releases the pages of slots[i] and empties the slot.
  *   fork     dst[i] (an empty slot) becomes a copy of src[i]: it shares the pages of the committed rows. Sources
  *            are read as they were before the call; a source that is also a destination is refused.
@@ -392,7 +393,9 @@ HA_API int hyper_attn_tree(hyper_attn_t h, const ha_cache *cache, const ha_tree_
  *            whose page is missing or shared (no reserve since the fork) is left out and reported.
  *   commit   keeps counts[i] of the rows behind the committed ones: row length + keep[i][j] moves to
  *            length + j (keep [n, max_keep], strictly ascending in each row's first counts[i] entries; NULL: the
- *            first counts[i] rows, nothing moves), the length grows by counts[i], pages behind it are released. */
+ *            first counts[i] rows, nothing moves), the length grows by counts[i], pages behind it are released. With
+ *            keep, an entry whose rows would go to a page that another slot shares (a fork since the reserve) is
+ *            left out and reported. */
 HA_API int hyper_attn_cache_free(hyper_attn_t h, const ha_cache *cache, const int32_t *slots, int64_t n);
 HA_API int hyper_attn_cache_fork(hyper_attn_t h, const ha_cache *cache, const int32_t *src, const int32_t *dst, int64_t n);
 HA_API size_t hyper_attn_cache_workspace(int64_t n, int64_t pages);

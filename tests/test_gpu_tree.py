@@ -268,9 +268,10 @@ def test_rows_that_see_nothing(ha, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("value", [float("inf"), float("nan")])
-def test_not_finite_in_masked_drafts(ha, dtype, value):
+@pytest.mark.parametrize("d", [64, 128])
+def test_not_finite_in_masked_drafts(ha, dtype, value, d):
     """A drafted row that is not finite reaches the tokens that see it and no other."""
-    lens, drafts, d = [100], [6], 64
+    lens, drafts = [100], [6]
     f = Filled(lens, drafts, page=16, hk=1, d=d, dtype=dtype, seed=8)
     masks = [1, 2, 5, 9, 16, 33]
     at = 102                         # drafted row 2, seen by token 2 alone
@@ -333,12 +334,13 @@ def test_bad_state_is_left_out(ha, dtype, fault):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("bad", [-1, -2 ** 31, 10 ** 6, 2 ** 31 - 1])
-def test_bad_pages_are_reported(ha, dtype, bad):
+@pytest.mark.parametrize("d", [64, 128])
+def test_bad_pages_are_reported(ha, dtype, bad, d):
     """A page out of range in one sequence: nothing is read there, the call reports it, the other sequences are right."""
     lens, drafts = [30, 200, 17], [4, 3, 5]
-    f = Filled(lens, drafts, page=16, hk=2, d=64, dtype=dtype, seed=6)
+    f = Filled(lens, drafts, page=16, hk=2, d=d, dtype=dtype, seed=6)
     f.cache.table[f.order[1], 4] = bad
-    q = torch.randn(12, 4, 64, generator=torch.Generator().manual_seed(2)).to(DT[dtype])
+    q = torch.randn(12, 4, d, generator=torch.Generator().manual_seed(2)).to(DT[dtype])
     options(ha, dtype)
     O = torch.full_like(q, 5.0, device="cuda")
     ha.tree(q.cuda(), f.cache, O, ints(f.order), ints(offsets_of(drafts)), max_draft=5, layer=1, scale=0.125)
@@ -586,6 +588,42 @@ def test_append_does_not_write_a_shared_page(ha):
     assert c.table.tolist() == [[0, 1, -1], [0, 2, -1]]
 
 
+def test_append_takes_a_slot_once(ha):
+    """The second entry of a slot is left out and reported, at the front and behind more entries than a block has threads."""
+    options(ha, "fp32")
+    n = 700
+    c = binding.PagedCache.empty(layers=1, pages=n, kv_heads=1, page=16, d=64, slots=n, max_pages=1, dtype="fp32")
+    ha.cache_reserve(c, ints(list(range(n))), ints([2] * n))
+    who = list(range(n))
+    who[1], who[n - 1] = 0, 300
+    row = torch.arange(1, 2 * n + 1, device="cuda").float()[None, :, None, None].repeat(1, 1, 1, 64)
+    ha.cache_append(c, ints(who), ints(list(range(0, 2 * n + 1, 2))), row, row)
+    assert ha.status() == binding.HA_ERR_INVALID_ARG and ha.status() == 0
+    want = torch.arange(1, 2 * n + 1, device="cuda").float().view(n, 2)
+    want[[1, n - 1]] = 0
+    for x in (c.k, c.v):
+        assert torch.equal(x[0, c.table[:, 0].long(), 0, :2, 5], want)
+
+
+def test_commit_does_not_write_a_shared_page(ha):
+    """Slot 1 is forked from slot 0, then slot 0 commits drafted rows of the page that both hold."""
+    options(ha, "bf16")
+    c = binding.PagedCache.empty(layers=1, pages=6, kv_heads=1, page=16, d=64, slots=2, max_pages=3)
+    row = torch.randn(1, 6, 1, 64, device="cuda").to(torch.bfloat16)
+    ha.cache_reserve(c, ints([0]), ints([6]))
+    ha.cache_append(c, ints([0]), ints([0, 6]), row, row)
+    ha.cache_commit(c, ints([0]), ints([2]))
+    ha.cache_fork(c, ints([0]), ints([1]))
+    ha.cache_commit(c, ints([0]), ints([1]))                                # nothing moves: rows 0..2 of the page
+    assert ha.status() == 0 and c.lens.tolist() == [3, 2]
+    before = c.k.clone()
+    ha.cache_commit(c, ints([1]), ints([1]), ints([[1]]))                   # would write slot 0's row 2
+    assert ha.status() == binding.HA_ERR_INVALID_ARG and ha.status() == 0
+    assert torch.equal(c.k, before) and c.lens.tolist() == [3, 2]
+    ha.cache_commit(c, ints([1]), ints([0]), ints([[1]]))
+    assert ha.status() == 0 and c.lens.tolist() == [3, 2] and torch.equal(c.k, before)
+
+
 def test_empty_lists_and_graph_of_steps(ha):
     """Lists of no entries do nothing; a captured cycle of all steps gives the same state at every replay."""
     side = torch.cuda.Stream()
@@ -691,6 +729,9 @@ def test_cache_refusals(ha):
     assert L.hyper_attn_cache_free(ha._h, c.args, None, 1) == inv
     assert L.hyper_attn_cache_free(ha._h, c.args, None, -1) == inv
     assert L.hyper_attn_cache_free(ha._h, c.args, None, 0) == 0
+    for call, most in ((L.hyper_attn_cache_free, 16384), (L.hyper_attn_cache_append, 65536)):
+        more = (most + 1,) if call is L.hyper_attn_cache_free else (None, most + 1, 1, None, None, None, None, 0, 1)
+        assert call(ha._h, c.args, None, *more) == inv
     assert L.hyper_attn_cache_reserve(ha._h, c.args, c.lens.data_ptr(), c.lens.data_ptr(), 1, None, None, 0) == inv
     assert L.hyper_attn_cache_commit(ha._h, c.args, c.lens.data_ptr(), c.lens.data_ptr(), c.lens.data_ptr(), 0, 1) == inv
     assert ha.status() == 0
