@@ -85,8 +85,8 @@ struct Cfg {
     static constexpr int kQ = 0;
     static constexpr int kK = NQ * kTile;
     static constexpr int kV = kK + NK * kTile;
-    static constexpr int kOut = kV + NV * kTile;                   // PAIR: 32 rows of 128 bytes per epilogue warp
-    static constexpr int kItemsAt = kOut + 4 * (ALT ? 0 : 4096);
+    static constexpr int kOut = kV + NV * kTile;                   // PAIR: 32 rows of O in bf16 per epilogue warp
+    static constexpr int kItemsAt = kOut + 4 * (ALT ? 0 : 64 * D);
     static constexpr int kStat = kItemsAt + kItems * 64;           // maximum and sum of the tiles' rows
     static constexpr int kBars = kStat + 2 * 128 * 8;
     static constexpr int bQFull = 0, bQEmpty = bQFull + 2, bKFull = bQEmpty + 2, bKEmpty = bKFull + NK,
@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
             piece[ALT ? 0 : e] = tk * a.o_tok + (rr - tk * a.group) * a.o_head + (lane & 7) * 8;
         }
         const float2 *stat = reinterpret_cast<const float2 *>(sm + C::kStat);
-        unsigned char *stage = sm + C::kOut + q * 4096;
+        unsigned char *stage = sm + C::kOut + q * 64 * D;
         constexpr int kPartRows = ALT ? 128 : 256;
         uint32_t done = 0;   // parities, bit t: items of tile t
         bool ok = true;
@@ -987,26 +987,32 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                             // through shared memory: a thread has a row, but a warp's store should cover whole 128-byte pieces
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                                *reinterpret_cast<uint4 *>(stage + h * 4096 + lane * 128 + ((e ^ (lane & 7)) << 4)) =
                                     make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-                            __syncwarp();
-                            uint4 v[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int rr = e * 4 + (lane >> 3);
-                                v[e] = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-                            }
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (q * 32 + e * 4 + (lane >> 3) < rows)
-                                    *reinterpret_cast<uint4 *>(tile_out + piece[ALT ? 0 : e] + h * 64) = v[e];
-                            __syncwarp();
                         } else if (mine) {
                             // few rows: straight from the threads
                             uint4 *dst = reinterpret_cast<uint4 *>(tile_out + my_off + h * 64);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                         }
+                    }
+                    // the stores come last: the next item waits for O
+                    if (!ALT) {
+                        __syncwarp();
+#pragma unroll 1
+                        for (int h = 0; h < D / 64; ++h) {
+                            uint4 v[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int rr = e * 4 + (lane >> 3);
+                                v[e] = *reinterpret_cast<const uint4 *>(stage + h * 4096 + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                            }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (q * 32 + e * 4 + (lane >> 3) < rows)
+                                    *reinterpret_cast<uint4 *>(tile_out + piece[ALT ? 0 : e] + h * 64) = v[e];
+                        }
+                        __syncwarp();
                     }
                 } else {
                     // fp32 rows: of the output, or of a piece's numerators

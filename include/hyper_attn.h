@@ -303,8 +303,9 @@ HA_API int hyper_attn_forward_noalloc(const void *Q, const void *K, const void *
  *     at most 128 query heads share one key head; query head h reads key head h / (heads / kv_heads).
  *   - `scale` (> 0) multiplies q.k inside exp.
  *   - Offsets, lengths, slots, masks and page tables are device memory and are read when the kernels run. An
- *     entry out of range leaves its sequence out (nothing of it is written) and makes hyper_attn_status report
- *     HA_ERR_INVALID_ARG; nothing is read or written out of bounds.
+ *     entry out of range leaves its sequence out (nothing of it is written; a page out of range in an attention call
+ *     counts as rows of zeros) and makes hyper_attn_status report HA_ERR_INVALID_ARG; nothing is read or written out
+ *     of bounds.
  *   - A row that sees nothing gives O = 0 and a log normaliser of -inf; so does one whose scores are all -inf
  *     over finite values. Infinities and NaN in keys and values that a row does not see do not reach it.
  *   - Rows of O (and of the log normalisers) behind the last sequence are left as they are.
