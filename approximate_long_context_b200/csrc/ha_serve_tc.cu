@@ -683,23 +683,29 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                 if (!warp_wait(bar(C::bVFull + s), (nv / C::NV) & 1)) { ok = false; break; }
                 if (it->k0 + (duo ? j >> 1 : j) >= it->masked) {
                     uint4 *tile = reinterpret_cast<uint4 *>(sm + C::kV + s * C::kTile);
+                    // an exponent of ones in either half carries into the bit above it
+                    auto bad = [](uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
                     bool odd = false;
-#pragma unroll 4
-                    for (int e = (warp - 2) * 32 + lane; e < C::kTile / 16; e += 64) {
-                        uint4 w = tile[e];
-                        // an exponent of ones in either half carries into the bit above it
-                        auto bad = [](uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
-                        if (bad(w.x) | bad(w.y) | bad(w.z) | bad(w.w)) {
+#pragma unroll 1
+                    for (int e0 = (warp - 2) * 32 + lane; e0 < C::kTile / 16; e0 += 64 * 8) {
+                        // eight loads in flight, with no store between them (256 short prompts: 55.9 -> 53.1 us, 16 ragged ones: 234.6 -> 230.3)
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint4 w = tile[e0 + e * 64];
+                            any |= bad(w.x) | bad(w.y) | bad(w.z) | bad(w.w);
+                        }
+                        if (any) {
+                            odd = true;
                             auto clean = [&](uint32_t u) {
                                 const uint32_t b = bad(u);
                                 return u & ~((b & 0x80000000u ? 0xffff0000u : 0u) | (b & 0x8000u ? 0xffffu : 0u));
                             };
-                            w.x = clean(w.x);
-                            w.y = clean(w.y);
-                            w.z = clean(w.z);
-                            w.w = clean(w.w);
-                            tile[e] = w;
-                            odd = true;
+#pragma unroll 1
+                            for (int e = 0; e < 8; ++e) {
+                                const uint4 w = tile[e0 + e * 64];
+                                tile[e0 + e * 64] = make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w));
+                            }
                         }
                     }
                     if (odd) it->odd = 1;
