@@ -75,9 +75,6 @@ class CacheArgs(ctypes.Structure):
                 [(n, ctypes.c_int) for n in ("kv_heads", "page", "d")])
 
 
-_STRIDES = ctypes.c_int64 * 3
-
-
 class TreeArgs(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "o", "lse")] + [("tokens", ctypes.c_int64)] +
                 [(n, ctypes.c_int64) for n in ("q_token", "q_head", "o_token", "o_head")] +
@@ -136,8 +133,7 @@ def lib():
     L.hyper_attn_cache_workspace.argtypes = [i64, i64]
     L.hyper_attn_cache_workspace.restype = st
     L.hyper_attn_cache_reserve.argtypes = [vp, cache, vp, vp, i64, vp, vp, st]
-    strides = ctypes.POINTER(ctypes.c_int64)
-    L.hyper_attn_cache_append.argtypes = [vp, cache, vp, vp, i64, i64, vp, vp, strides, strides, i64, i64]
+    L.hyper_attn_cache_append.argtypes = [vp, cache, vp, vp, i64, i64, vp, vp, ctypes.c_char_p, ctypes.c_char_p, i64, i64]
     L.hyper_attn_cache_commit.argtypes = [vp, cache, vp, vp, vp, i64, i64]
     # the same entry points taking the argument struct as packed bytes
     L.prompt_packed = L["hyper_attn_prompt"]
@@ -195,6 +191,8 @@ def _need(ok: bool, what: str):
 # field takes several times as long, and these calls run once per layer and token.
 _PROMPT = struct.Struct("@5Pq8q3iPqqfPN")
 _TREE = struct.Struct("@3Pq4qiq3PqifPN")
+_APPEND = struct.Struct("@3q")
+_CACHE = struct.Struct("@6P4q3i4x")
 _torch = None
 
 
@@ -232,9 +230,10 @@ class PagedCache:
         self.k, self.v, self.table, self.lens, self.held, self.refs = k, v, table, lens, held, refs
         self.device, self.dtype = device, k.dtype
         self.pages, self.kv_heads, self.page, self.d = pages, kv_heads, page, d
-        self.args = CacheArgs(k.data_ptr(), v.data_ptr(), _ints(table, device, "table"), _ints(lens, device, "lens", slots),
-                              _ints(held, device, "held", slots), _ints(refs, device, "refs", pages), layers, pages, slots,
-                              max_pages, kv_heads, page, d)
+        self.args = CacheArgs.from_buffer_copy(_CACHE.pack(
+            k.data_ptr(), v.data_ptr(), _ints(table, device, "table"), _ints(lens, device, "lens", slots),
+            _ints(held, device, "held", slots), _ints(refs, device, "refs", pages), layers, pages, slots, max_pages, kv_heads,
+            page, d))
 
     @classmethod
     def empty(cls, *, layers, pages, kv_heads, page, d, slots, max_pages, dtype="bf16", device=0):
@@ -458,7 +457,7 @@ class HyperAttention:
             s = t.stride()
             if len(s) != 4 or (s[3] != 1 and t.shape[3] != 1) or t.dtype is not cache.dtype or t.get_device() != self.device:
                 raise ValueError("K, V: [layers, tokens, kv_heads, d] of the cache's type on the handle's device, contiguous rows")
-            strides.append(_STRIDES(*s[:3]))
+            strides.append(_APPEND.pack(s[0], s[1], s[2]))
         shape = K.shape
         if V.shape != shape or shape[2] != cache.kv_heads or shape[3] != cache.d:
             raise ValueError("K, V: the cache's kv_heads and d are needed")

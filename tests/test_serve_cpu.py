@@ -37,7 +37,8 @@ def test_structs_mirror_the_header(tmp_path, c, py):
         assert int(out[f]) == getattr(py, f).offset, f
 
 
-@pytest.mark.parametrize("packed,py", [(binding._PROMPT, binding.PromptArgs), (binding._TREE, binding.TreeArgs)])
+@pytest.mark.parametrize("packed,py", [(binding._PROMPT, binding.PromptArgs), (binding._TREE, binding.TreeArgs),
+                                       (binding._CACHE, binding.CacheArgs)])
 def test_packed_arguments_are_the_struct(packed, py):
     values = list(range(3, 3 + len(py._fields_)))
     raw = packed.pack(*values)
