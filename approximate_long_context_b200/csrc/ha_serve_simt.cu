@@ -11,6 +11,10 @@
 //
 // A value row of a masked key can hold an infinity or NaN and must not reach the rows that do not see it (0 * inf):
 // the load of a tile votes on non-finite values, and a tile with one and a mask takes the product with a select.
+//
+// What bounds it: shared-memory loads (81% of their rate, the FMA pipes 33% in packed instructions). 8192 tokens, 8 heads on
+// 4: 36.7 TFLOP/s at d = 64, 39.2 at d = 128. Decoding over an fp32 cache (32 users x 8192 rows, d = 64) takes
+// tree_few_kernel: 165 us (3.25 TB/s) against 317 us here, where 64-row tiles multiply mostly nothing.
 #include <math.h>
 
 #include <atomic>

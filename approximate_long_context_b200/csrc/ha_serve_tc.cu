@@ -9,8 +9,8 @@
 //         small trees, which are bound by reading the cache).
 //   ALT16: ALT for d = 128 and pages of 16 rows. A load of a page brings one box of 64 columns; with 2 KB boxes the copy
 //         engine and not the memory is the bound (64 users decoding: 424 us, against 330 us with larger pages and 342 us
-//         here; 16 trees of 32 tokens: 100 -> 83 us). Here a box has both halves of the page's rows (4 KB). A key tile then lies page by page, [half][16 rows][128 bytes], which
-//         the score product reads as two products of 64 keys, rows 0-7 and rows 8-15 of the eight pages; the softmax
+//         here; 16 trees of 32 tokens: 100 -> 83 us). Here a box has both halves of the page's rows (4 KB). A key
+//         tile then lies page by page, [half][16 rows][128 bytes], which the score product reads as two products of 64 keys, rows 0-7 and rows 8-15 of the eight pages; the softmax
 //         puts the keys back in order when it writes P.
 // Tree items come from an even cut of all key tiles over the blocks (TreeWalk); pieces of a cut segment go to the
 // workspace and a second kernel joins them.
@@ -32,6 +32,13 @@
 // and 3 look values over, warps 4-7 and 8-11 are the softmax of tile 0 and 1, warps 12-15 the epilogue of both (a tile's
 // epilogue takes as long as one or two of its units; the softmax goes on with the next item meanwhile). Every wait is
 // bounded; on expiry the status word is set, all roles stop, the loader waits for its copies and TMEM is freed.
+//
+// What bounds it. Prompts: per tile and unit (128 rows x 128 keys, d = 128) the softmax takes about 1900 cycles and P V
+// with the next S another 1600, of which 1024 are the tensor pipe's; two tiles overlap, so tensor pipe and exponentials
+// are busy 59% each, and TMEM has no room for a third tile. 32768 tokens, 8 heads on 2, d = 128: 1.76 ms (1250 TFLOP/s; 2.00
+// ms under sustained power). 16 prompts of up to 2047 tokens, 32 heads on 8: 230 us (870 TFLOP/s). Prompts of one key
+// tile (256 of up to 128 tokens, 16 heads, d = 64: 53 us, 2.5 TB/s): instruction fetch, each role's code runs once per
+// item. Decoding and small trees: reading the cache, 64 users and 2.2 GB: 330 us (6.6 TB/s).
 #include <cuda.h>
 #include <math.h>
 
@@ -688,7 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
                     bool odd = false;
 #pragma unroll 1
                     for (int e0 = (warp - 2) * 32 + lane; e0 < C::kTile / 16; e0 += 64 * 8) {
-                        // eight loads in flight, with no store between them (256 short prompts: 55.9 -> 53.1 us, 16 ragged ones: 234.6 -> 230.3)
+                        // eight loads in flight, with no store between them (256 short prompts: 55.9 -> 53.1 us, 16
+                        // ragged ones: 234.6 -> 230.3 us)
                         uint32_t any = 0;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
