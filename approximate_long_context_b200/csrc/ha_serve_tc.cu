@@ -10,8 +10,9 @@
 //   ALT16: ALT for d = 128 and pages of 16 rows. A load of a page brings one box of 64 columns; with 2 KB boxes the copy
 //         engine and not the memory is the bound (64 users decoding: 424 us, against 330 us with larger pages and 342 us
 //         here; 16 trees of 32 tokens: 100 -> 83 us). Here a box has both halves of the page's rows (4 KB). A key
-//         tile then lies page by page, [half][16 rows][128 bytes], which the score product reads as two products of 64 keys, rows 0-7 and rows 8-15 of the eight pages; the softmax
-//         puts the keys back in order when it writes P.
+//         tile then lies page by page, [half][16 rows][128 bytes], which the score product reads as two products of
+//         64 keys, rows 0-7 and rows 8-15 of the eight pages; the softmax puts the keys back in order when it
+//         writes P.
 // Tree items come from an even cut of all key tiles over the blocks (TreeWalk); pieces of a cut segment go to the
 // workspace and a second kernel joins them.
 //
