@@ -163,6 +163,9 @@ size_t serve_tree_workspace(int sms, int d);
 int launch_prompt_simt(const ServeArgs &a, int dtype, cudaStream_t st);
 int launch_tree_simt(const ServeArgs &a, int dtype, cudaStream_t st);
 int launch_prompt_tc(const ServeArgs &a, cudaStream_t st);
+// A few short prompts in bf16 (launch_prompt_tc asks): no workspace.
+bool prompt_is_short(const ServeArgs &a);
+int launch_prompt_short(const ServeArgs &a, cudaStream_t st);
 int launch_tree_tc(const ServeArgs &a, cudaStream_t st);
 // The second kernel of a tree call on `blocks` blocks whose segments have at most `rows` query rows.
 bool launch_tree_join(const ServeArgs &a, int blocks, int rows, cudaStream_t st);

@@ -1170,6 +1170,7 @@ size_t prompt_tc_workspace(int64_t tokens, int64_t seqs, int64_t max_len, int kv
 }
 
 int launch_prompt_tc(const ServeArgs &a, cudaStream_t st) {
+    if (prompt_is_short(a)) return launch_prompt_short(a, st);
     TcArgs x{};
     x.a = a;
     x.tpt = 128 / a.group;

@@ -74,6 +74,61 @@ def test_prompt_matches_definition(ha, kind, d, heads, lens):
     verify(q, k, v, O, lse, lens, d ** -0.5, UBF if kind in ("bf16", "bf16_to_fp32") else None, out_bf16)
 
 
+@pytest.mark.parametrize("d,most", [(64, 128), (64, 15), (128, 64), (128, 33)])
+@pytest.mark.parametrize("group", [1, 3, 16, 128])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_a_few_short_prompts(ha, d, most, group, out):
+    """Calls of one round of small blocks: strided rows, lengths around 16 and 64, rows behind the last sequence."""
+    lens = [n for n in (1, 0, 15, 16, 17, 33, 63, 64, 65, 127, 128) if n <= most]
+    if group == 128:
+        lens = [1, 0, 17] if most > 16 else [1, 0, 15]
+    hk = 2 if group < 16 else 1
+    total = sum(lens)
+    q, k, v = make(total + 3, hk * group, hk, d, "bf16", seed=d + group)
+    k[total:], v[total:] = float("nan"), float("inf")
+    wide = torch.randn(total + 3, hk * group, d + 8).to(torch.bfloat16).cuda()
+    Q = wide[:, :, :d]
+    Q.copy_(q)
+    options(ha, "bf16", out_dtype=out)
+    whole = torch.full((hk * group, total + 3, d), 7.0, dtype=DT[out], device="cuda")
+    O = whole.transpose(0, 1)
+    lse = torch.full((hk * group, total + 3), 7.0, device="cuda")
+    cu = torch.tensor(offsets_of(lens), dtype=torch.int32, device="cuda")
+    ha.prompt(Q, k.cuda(), v.cuda(), O, cu, max_len=max(lens), scale=d ** -0.5, lse=lse)
+    assert ha.status() == 0, ha.last_error()
+    verify(q, k, v, O, lse, lens, d ** -0.5, UBF, out == "bf16")
+    assert bool((O[total:] == 7).all()) and bool((lse[:, total:] == 7).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("at", [0, 7, 15, 16, 40, 62])
+def test_not_finite_in_short_prompts(ha, d, value, at):
+    n = 63
+    q, k, v = make(n, 6, 2, d, "bf16", seed=at)
+    clean = v.clone()
+    v[at, 1, 5] = value
+    options(ha, "bf16")
+    O = torch.empty_like(q, device="cuda")
+    lse = torch.empty(6, n, device="cuda")
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    ha.prompt(q.cuda(), k.cuda(), v.cuda(), O, cu, scale=0.125, lse=lse)
+    assert ha.status() == 0, ha.last_error()
+    hit = O[at:, 3:, 5].clone()
+    assert bool(torch.isnan(hit.float()).all()) if value != value else bool((hit.float() == value).all())
+    # elsewhere it is the clean answer
+    want = torch.empty_like(O)
+    ha.prompt(q.cuda(), k.cuda(), clean.cuda(), want, cu, scale=0.125)
+    O[at:, 3:, 5] = want[at:, 3:, 5]
+    assert torch.equal(O, want)
+    verify(q, k, clean, O, lse, [n], 0.125, UBF, True)
+    k[at, 0, 3] = float("nan")
+    ha.prompt(q.cuda(), k.cuda(), clean.cuda(), O, cu, scale=0.125)
+    assert bool(torch.isnan(O[at:, :3].float()).all())
+    O[at:, :3] = want[at:, :3]
+    assert torch.equal(O, want)
+
+
 def random_lens(n, most, seed, empty=0.1):
     import random
     rng = random.Random(seed)
