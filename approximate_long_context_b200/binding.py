@@ -182,11 +182,6 @@ def _ptr(x) -> int:
     return int(x)
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
 # The argument structs of the serving calls are packed with `struct` (native alignment): filling a ctypes Structure field by
 # field takes several times as long, and these calls run once per layer and token.
 _PROMPT = struct.Struct("@5Pq8q3iPqqfPN")
@@ -260,6 +255,7 @@ class HyperAttention:
         self._device_object = None
         self._ws, self._ws_ptr, self._ws_bytes = None, 0, 0
         self._captured = []
+        self._needs = {}
 
     def _check(self, rc: int):
         if rc:
@@ -282,6 +278,7 @@ class HyperAttention:
         if o.stream != self.options.stream:   # the buffer's reuse was ordered by the old stream
             self._ws, self._ws_ptr, self._ws_bytes = None, 0, 0
         self.options = o
+        self._needs.clear()
 
     def forward(self, Q, K, V, O, *, n, d, heads, block, m, r, causal, seed):
         """Device tensors (torch CUDA tensors or raw device addresses)."""
@@ -325,6 +322,15 @@ class HyperAttention:
         if t.get_device() != self.device:
             raise ValueError(f"{what}: on the handle's device")
         return t.data_ptr(), stride[0], stride[1]
+
+    def _need(self, ask, sizes) -> int:
+        """The workspace of a call with these sizes under the options as they are; the library is asked once."""
+        nbytes = self._needs.get(sizes)
+        if nbytes is None:
+            if len(self._needs) >= 256:
+                self._needs.clear()
+            nbytes = self._needs[sizes] = ask(self._h, *sizes)
+        return nbytes
 
     def _workspace(self, nbytes: int) -> int:
         """The address of a device buffer of at least nbytes. Eager calls share one, in the order of the handle's stream; a
@@ -382,7 +388,7 @@ class HyperAttention:
         L = _lib
         if max_len is None:
             max_len = max(tokens, 1)
-        nbytes = L.hyper_attn_prompt_workspace(self._h, tokens, seqs, max_len, heads, kv_heads)
+        nbytes = self._need(L.hyper_attn_prompt_workspace, (tokens, seqs, max_len, heads, kv_heads))
         ws = self._workspace(nbytes)
         rc = L.prompt_packed(self._h, _PROMPT.pack(
             q[0], k[0], v[0], o[0], self._lse(lse, heads, tokens) or 0, tokens, q[1], q[2], k[1], k[2], v[1], v[2], o[1], o[2],
@@ -410,7 +416,7 @@ class HyperAttention:
         at = _ints(offsets, self.device, "offsets")
         seqs = offsets.numel() - 1
         L = _lib
-        nbytes = L.hyper_attn_tree_workspace(self._h, d)
+        nbytes = self._need(L.hyper_attn_tree_workspace, (d,))
         ws = self._workspace(nbytes)
         rc = L.tree_packed(self._h, c, _TREE.pack(
             q[0], o[0], self._lse(lse, heads, tokens) or 0, tokens, q[1], q[2], o[1], o[2], heads, layer,
