@@ -8,7 +8,7 @@
 //
 // What bounds these kernels: the row traffic (each row read once and written once, 16 bytes per thread) for large
 // calls, launch latency and the chain of dependent loads (slot -> length -> page -> row) for small ones. All five steps for
-// 64 branches of 8 prompts (drafts of up to 16, 32 layers, 8 heads, d = 128): 76 us against 51 us for the rows' bytes at the
+// 64 branches of 8 prompts (drafts of up to 16, 32 layers, 8 heads, d = 128): 69 us against 51 us for the rows' bytes at the
 // memory's rate; for two branches in one layer: 16.5 us, five launches.
 #include "ha_common.cuh"
 #include "ha_internal.h"
@@ -147,16 +147,16 @@ __device__ __forceinline__ void copy_page(const ServeCache &c, int esz, char *ba
     const int total = per_head * c.kv_heads;
     for (int x0 = threadIdx.x; x0 < total; x0 += THREADS * 4) {
         int4 buf[4];
+        int64_t off[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int x = x0 + THREADS * u;
-            if (x < total) buf[u] = *reinterpret_cast<const int4 *>(src + (x / per_head) * head_bytes + (x % per_head) * 16);
+            const int x = x0 + THREADS * u, h = x / per_head;
+            off[u] = h * head_bytes + (x - h * per_head) * 16;
+            if (x < total) buf[u] = *reinterpret_cast<const int4 *>(src + off[u]);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int x = x0 + THREADS * u;
-            if (x < total) *reinterpret_cast<int4 *>(dst + (x / per_head) * head_bytes + (x % per_head) * 16) = buf[u];
-        }
+        for (int u = 0; u < 4; ++u)
+            if (x0 + THREADS * u < total) *reinterpret_cast<int4 *>(dst + off[u]) = buf[u];
     }
 }
 
@@ -322,7 +322,7 @@ struct AppendArgs {
     int64_t layer, layers;
 };
 
-constexpr int kAppendLayers = 4;   // layers per block
+constexpr int kAppendLayers = 8;   // layers per block (4: 1.3% slower for a whole branch step of 32 layers, 16: as 8)
 
 // One block per token and group of layers: the place is looked up once, then the rows are copied.
 __global__ void __launch_bounds__(256) cache_append_kernel(const ServeCache c, int esz, const int32_t *slots,
@@ -368,25 +368,28 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const ServeCache c, i
     }
     const int64_t row_bytes = static_cast<int64_t>(c.d) * esz, head_bytes = row_bytes * c.page,
                   page_bytes = head_bytes * c.kv_heads;
-    const int per_row = static_cast<int>(row_bytes / 16), per_layer = per_row * c.kv_heads;
     const int64_t l0 = static_cast<int64_t>(blockIdx.y) * kAppendLayers;
     const int nl = static_cast<int>(min(static_cast<int64_t>(kAppendLayers), a.layers - l0));
-    const int total = per_layer * nl * 2;
-    const int64_t off = (at & (c.page - 1)) * row_bytes;
-    for (int x0 = threadIdx.x; x0 < total; x0 += 256 * 4) {
+    const int rows = 2 * nl * c.kv_heads;          // of k in all layers, then of v
+    // a thread has one 16-byte piece of every (256 / pieces)-th row; pieces is 8, 16 or 32
+    const int shift = 31 - __clz(static_cast<int>(row_bytes / 16));
+    const int piece = (threadIdx.x & ((1 << shift) - 1)) * 16, step = 256 >> shift;
+    const char *const k = a.k + l0 * a.kl + t * a.kt + piece, *const v = a.v + l0 * a.vl + t * a.vt + piece;
+    const int64_t layer_bytes = c.pages * page_bytes;
+    const int64_t off = (a.layer + l0) * layer_bytes + id * page_bytes + (at & (c.page - 1)) * row_bytes + piece;
+    for (int r0 = threadIdx.x >> shift; r0 < rows; r0 += step * 4) {
         int4 buf[4];
         char *dst[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int x = x0 + 256 * u;
+            const int r = r0 + step * u;
             dst[u] = nullptr;
-            if (x >= total) continue;
-            const int kv = x / (per_layer * nl), y = x - kv * per_layer * nl;
-            const int l = y / per_layer, z = y - l * per_layer, h = z / per_row, w = z - h * per_row;
-            const char *src = kv ? a.v + (l0 + l) * a.vl + t * a.vt + h * a.vh : a.k + (l0 + l) * a.kl + t * a.kt + h * a.kh;
-            buf[u] = *reinterpret_cast<const int4 *>(src + w * 16);
-            dst[u] = static_cast<char *>(kv ? c.v : c.k) + ((a.layer + l0 + l) * c.pages + id) * page_bytes +
-                     h * head_bytes + off + w * 16;
+            if (r >= rows) continue;
+            const int y = r / c.kv_heads, h = r - y * c.kv_heads;
+            const bool second = y >= nl;
+            const int l = second ? y - nl : y;
+            buf[u] = *reinterpret_cast<const int4 *>(second ? v + l * a.vl + h * a.vh : k + l * a.kl + h * a.kh);
+            dst[u] = static_cast<char *>(second ? c.v : c.k) + l * layer_bytes + h * head_bytes + off;
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
