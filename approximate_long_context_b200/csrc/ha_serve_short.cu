@@ -1,13 +1,13 @@
-// ha_serve_short.cu -- attention over a few short prompts, bf16: for calls that end within one round of small blocks, where
-// the time of one chain counts.
+// ha_serve_short.cu -- attention over short packed prompts (at most 128 tokens), bf16: few of them, where the time of one
+// chain counts, and many that are much shorter than a tile.
 //
-// A block has 64 query rows (token * group + head) of a key head and all keys up to its last token (at most 128) in
-// shared memory; a warp has 16 rows and all their scores in registers: S = Q K^T by mma.sync (m16n8k16), a plain
-// softmax, O = P V. No tensor maps on the host, no TMEM, no hand-over between warps.
+// A block has 64 query rows (token * group + head) of a key head and all keys up to its last token in shared memory; a
+// warp has 16 rows and all their scores in registers: S = Q K^T by mma.sync (m16n8k16), a plain softmax, O = P V. No tensor
+// maps on the host, no TMEM, no hand-over between warps; several blocks per SM hide one another's loads.
 //
 // What bounds it: the chain offsets -> rows -> products. One prompt of 77 tokens, 8 heads on 2, d = 64: 4.7 us against 6.9 us
-// in the persistent tcgen05 kernel; 16 prompts of 128 tokens, 16 heads, d = 64 (512 blocks): 8.7 us both; 64 of them: 29
-// against 18 us, as mma.sync multiplies at a fraction of tcgen05's rate.
+// in the persistent tcgen05 kernel; 256 of up to 32 tokens, 16 heads, d = 64: 26 us against 48; but 256 of up to 128
+// tokens: 71 against 52, as mma.sync multiplies at a fraction of tcgen05's rate.
 //
 // The weights are rounded to bf16 because the tensor core multiplies bf16; the normaliser sums the unrounded values.
 // Values of keys that a row does not see may be infinities or NaN: in the 16 keys at the diagonal what is not finite is
@@ -272,16 +272,23 @@ bool launch(const ServeArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-// Where this kernel is the faster one, in us here and there (8 heads on 2 and 16 heads at d = 64, 32 on 8 at d = 128):
-// d = 64, 128 tokens: 256 blocks 7.3 and 8.4, 512 blocks 8.7 and 8.7 to 11.2, 1024 blocks 15.7 and 11.6;
-// d = 64, 32 tokens: 512 blocks 5.2 and 11.2, 1024 blocks 8.7 and 16.7;
-// d = 128, 32 tokens: 256 blocks 6.5 and 9.3, 512 blocks 10.9 and 9.7; 128 tokens: 64 blocks 9.7 and 9.5.
-// The products grow with blocks, keys and d, and half as many blocks fit on an SM at d = 128.
+// Where this kernel is the faster one, in us here and there:
+// - one round of blocks (8 heads on 2 and 16 heads at d = 64, 32 on 8 at d = 128): d = 64, 128 tokens: 256 blocks 7.3 and 8.4,
+//   512 blocks 8.7 and 8.7 to 11.2, 1024 blocks 15.7 and 11.6; d = 64, 32 tokens: 512 blocks 5.2 and 11.2; d = 128, 32 tokens:
+//   256 blocks 6.5 and 9.3, 512 blocks 10.9 and 9.7; 128 tokens: 64 blocks 9.7 and 9.5;
+// - more of them: an SM takes about 0.7 + 0.0105 n us for a block of n keys at d = 64 and 1.9 + 0.022 n at d = 128, and 3.2 and
+//   4.2 us for an item of two query tiles there, full or not. 1024 prompts, 16 heads, d = 64, of 64 tokens: 148 and 182, of
+//   32: 118 and 175; 8 heads on 2 of 64: 71 and 55, of 16: 16 and 27; 32 heads on 8, d = 128, of 32: 294 and 139.
 bool prompt_is_short(const ServeArgs &a) {
-    if (a.max_len > kMaxKeys || a.max_len * a.d > kMaxKeys * 64) return false;
-    const int64_t blocks = static_cast<int64_t>(a.seqs) * a.kv_heads * ((a.max_len * a.group + kRows - 1) / kRows);
-    const int shorter = kMaxKeys * 64 / (a.max_len * a.d);   // than 128 tokens at d = 64, at least 1
-    return blocks <= 2 * a.sms * (shorter < 4 ? shorter : 4) * 64 / a.d;
+    if (a.max_len > kMaxKeys) return false;
+    const int64_t heads = static_cast<int64_t>(a.seqs) * a.kv_heads;
+    const int64_t blocks = heads * ((a.max_len * a.group + kRows - 1) / kRows);
+    if (blocks > 0x7fffffff) return false;
+    const int shorter = kMaxKeys * 64 / (a.max_len * a.d);   // than 128 tokens at d = 64
+    if (blocks <= 2 * a.sms * (shorter < 4 ? shorter : 4) * 64 / a.d) return true;
+    const int tokens = 128 / a.group;                        // of a query tile there
+    const int64_t items = a.max_len <= tokens ? (heads + 1) / 2 : heads * ((a.max_len + 2 * tokens - 1) / (2 * tokens));
+    return a.d == 64 ? blocks * (64 + a.max_len) < items * 288 : blocks * (86 + a.max_len) < items * 190;
 }
 
 int launch_prompt_short(const ServeArgs &a, cudaStream_t st) {

@@ -142,6 +142,8 @@ MANY = {
     "pairs": (300, 60, 2, 4),
     "singles": (400, 32, 2, 4),
     "singles_odd_heads": (200, 120, 3, 1),
+    "singles_even_heads": (200, 100, 2, 1),
+    "many_small_blocks": (700, 20, 6, 2),
     "few": (7, 200, 2, 1),
     "no_head_room": (170, 9, 1, 128),
     "thousands": (5000, 3, 1, 2),
