@@ -328,13 +328,17 @@ def _commit(st, slots):
 _handles = {}
 
 
-def _handle(dtype):
-    """The program's handle for a type, made once."""
-    if dtype not in _handles:
+def _handle(dtype, device):
+    """The program's handle for a type and device, made once; its calls go to the stream that is current."""
+    stream = torch._C._cuda_getCurrentRawStream(device)   # torch.cuda.current_stream takes 2 us
+    entry = _handles.get((dtype, device))
+    if entry is None:
         from approximate_long_context_b200 import binding
-        _handles[dtype] = binding.HyperAttention(torch.cuda.current_device())
-        _handles[dtype].set_options(dtype=dtype, stream=torch.cuda.current_stream().cuda_stream)
-    return _handles[dtype]
+        entry = _handles[dtype, device] = [binding.HyperAttention(device), None]
+    if entry[1] != stream:
+        entry[0].set_options(dtype=dtype, stream=stream)
+        entry[1] = stream
+    return entry[0]
 
 
 def _cache(st):
@@ -347,17 +351,19 @@ def run(st):
     if op == "prompt":
         if not own:
             return _prompt(st)
-        _handle(st["dtype"]).prompt(st["q"], st["k"], st["v"], st["o"], st["cu"], max_len=max(st["lengths"]),
-                                    scale=st["scale"], lse=st["lse"])
+        ha = _handle(st["dtype"], st["q"].get_device())
+        ha.prompt(st["q"], st["k"], st["v"], st["o"], st["cu"], max_len=max(st["lengths"]), scale=st["scale"], lse=st["lse"])
         return st["o"], st["lse"]
     if op == "tree":
         if not own:
             return _tree(st)
-        _handle(st["dtype"]).tree(st["q"], _cache(st), st["o"], st["seqs_at"], st["cu"], mask=st["mask"],
-                                  max_draft=st["draft"], scale=st["scale"], lse=st["lse"])
+        ha = _handle(st["dtype"], st["q"].get_device())
+        ha.tree(st["q"], _cache(st), st["o"], st["seqs_at"], st["cu"], mask=st["mask"], max_draft=st["draft"],
+                scale=st["scale"], lse=st["lse"])
         return st["o"], st["lse"]
     if own:
-        ha, cache = _handle(st["dtype"]), _cache(st)
+        cache = _cache(st)
+        ha = _handle(st["dtype"], cache.device)
         ha.cache_free(cache, st["dst"])
         ha.cache_fork(cache, st["src"], st["dst"])
         ha.cache_reserve(cache, st["dst"], st["add"], st["granted"])
