@@ -390,8 +390,9 @@ HA_API int hyper_attn_tree(hyper_attn_t h, const ha_cache *cache, const ha_tree_
  *            for the others, which are left as they were (status is not set for them).
  *            Workspace: hyper_attn_cache_workspace bytes.
  *   append   writes rows k, v [layers, tokens, kv_heads, d] (strides in elements: layer, token, head) to layers
- *            layer .. layer + layers - 1, row t of sequence i to its committed length + t. Lengths do not change. A row
- *            whose page is missing or shared (no reserve since the fork) is left out and reported.
+ *            layer .. layer + layers - 1, row t of sequence i to its committed length + t. Lengths do not change. A
+ *            sequence whose offsets are not rows of the call is left out and reported, and so is a row whose page is
+ *            missing or shared (no reserve since the fork). Rows of no sequence are passed over.
  *   commit   keeps counts[i] of the rows behind the committed ones: row length + keep[i][j] moves to
  *            length + j (keep [n, max_keep], strictly ascending in each row's first counts[i] entries; NULL: the
  *            first counts[i] rows, nothing moves), the length grows by counts[i], pages behind it are released. With
