@@ -52,7 +52,8 @@ __global__ void __launch_bounds__(256) cache_free_kernel(const ServeCache c, con
     }
 }
 
-// Sources are read as they were before the call: a source that is also a destination of the call is refused.
+// Sources are read as they were before the call: a source that is also a destination of the call is refused, and so is one whose
+// row of the table names a page out of range.
 __global__ void __launch_bounds__(256) cache_fork_kernel(const ServeCache c, const int32_t *src, const int32_t *dst, int n,
                                                          int *status) {
     grid_dependency_wait();
@@ -64,20 +65,22 @@ __global__ void __launch_bounds__(256) cache_fork_kernel(const ServeCache c, con
     int len = 0, pages = 0;
     if (!bad) {
         len = c.lens[s];
-        pages = (len + c.page - 1) >> c.page_shift;
-        bad = len < 0 || pages > c.held[s] || c.held[s] > c.max_pages || c.held[t] != 0 || c.lens[t] != 0;
+        const int held = c.held[s];
+        const int64_t need = (static_cast<int64_t>(len) + c.page - 1) >> c.page_shift;
+        bad = len < 0 || need > held || held > c.max_pages || c.held[t] != 0 || c.lens[t] != 0;
+        pages = bad ? 0 : static_cast<int>(need);
     }
-    __syncthreads();   // thread 0 writes the destination's length only after every thread has read it
-    if (bad) {
+    const int32_t *from = c.table + static_cast<int64_t>(s) * c.max_pages;
+    for (int p = threadIdx.x; p < pages; p += blockDim.x) bad |= from[p] < 0 || from[p] >= c.pages;
+    // from here on every thread has read the destination's length, which thread 0 writes
+    if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) atomicOr(status, kStatusData);
         return;
     }
-    const int32_t *from = c.table + static_cast<int64_t>(s) * c.max_pages;
     int32_t *to = c.table + static_cast<int64_t>(t) * c.max_pages;
     for (int p = threadIdx.x; p < pages; p += blockDim.x) {
         const int32_t id = from[p];
-        if (id >= 0 && id < c.pages) atomicAdd(c.refs + id, 1);
-        else atomicOr(status, kStatusData);
+        atomicAdd(c.refs + id, 1);
         to[p] = id;
     }
     if (threadIdx.x == 0) {

@@ -382,7 +382,8 @@ HA_API int hyper_attn_tree(hyper_attn_t h, const ha_cache *cache, const ha_tree_
  * range.
  *   free     releases the pages of slots[i] and empties the slot.
  *   fork     dst[i] (an empty slot) becomes a copy of src[i]: it shares the pages of the committed rows. Sources
- *            are read as they were before the call; a source that is also a destination is refused.
+ *            are read as they were before the call; a source that is also a destination is refused, and so is one
+ *            with a page out of range among those.
  *   reserve  makes room for add[i] more rows behind the committed ones of slots[i] (which replaces, not adds to, the
  *            room of an earlier reserve that was not committed): takes the lowest free pages, in list order, and
  *            replaces a shared, partly filled last page by a copy of its committed rows in all layers. The entries

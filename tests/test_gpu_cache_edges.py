@@ -1,4 +1,5 @@
-"""The cache's steps on lists that are not in order: offsets of an append that are out of range."""
+"""The cache's steps on lists and tables that are not in order: offsets of an append that are out of range, page numbers and
+lengths that a fork must not take over."""
 import pytest
 
 from approximate_long_context_b200 import binding
@@ -85,3 +86,41 @@ def test_append_rows_of_no_sequence(ha):
     got = c.k[0, c.table[:, 0].long(), 0, :4, 0].cpu()
     assert got.tolist() == [[3, 4, 5, 0], [6, 7, 0, 0]]
     assert c.k.abs().sum().item() == 64 * 25 and c.v.abs().sum().item() == 64 * 25
+
+
+def one_sequence():
+    """Slot 0 with 40 rows on three pages, slot 3 with 20 on two."""
+    return binding.PagedCache.empty(layers=1, pages=10, kv_heads=1, page=16, d=64, slots=5, max_pages=4, dtype="fp32")
+
+
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 10, 2 ** 31 - 1])
+@pytest.mark.parametrize("where", [0, 1, 2])
+def test_fork_of_a_damaged_row(ha, bad, where):
+    """A source whose row of the table has a page out of range is not forked, nor is any of its pages counted again."""
+    c = one_sequence()
+    ha.cache_reserve(c, ints([0, 3]), ints([40, 20]))
+    ha.cache_commit(c, ints([0, 3]), ints([40, 20]))
+    assert ha.status() == 0
+    c.table[0, where] = bad
+    refs = c.refs.tolist()
+    ha.cache_fork(c, ints([0, 3]), ints([1, 4]))
+    assert ha.status() == binding.HA_ERR_INVALID_ARG and ha.status() == 0
+    assert c.table[1].tolist() == [-1] * 4 and c.lens.tolist() == [40, 0, 0, 20, 20] and c.held.tolist() == [3, 0, 0, 2, 2]
+    want = list(refs)
+    for p in c.table[3, :2].tolist():
+        want[p] += 1
+    assert c.refs.tolist() == want and c.table[4].tolist() == c.table[3].tolist()
+
+
+@pytest.mark.parametrize("length", [-1, 49, 2 ** 31 - 15, 2 ** 31 - 1])
+def test_fork_of_a_damaged_length(ha, length):
+    c = one_sequence()
+    ha.cache_reserve(c, ints([0]), ints([40]))
+    ha.cache_commit(c, ints([0]), ints([40]))
+    assert ha.status() == 0
+    c.lens[0] = length
+    refs = c.refs.tolist()
+    ha.cache_fork(c, ints([0]), ints([1]))
+    assert ha.status() == binding.HA_ERR_INVALID_ARG and ha.status() == 0
+    assert c.lens.tolist() == [length, 0, 0, 0, 0] and c.held.tolist() == [3, 0, 0, 0, 0] and c.refs.tolist() == refs
+    assert c.table[1].tolist() == [-1] * 4
