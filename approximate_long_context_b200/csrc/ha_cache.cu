@@ -24,6 +24,7 @@ __device__ __forceinline__ bool block_contains(const int32_t *list, int n, int32
     return __syncthreads_or(hit);
 }
 
+// A page number out of range is reported and passed over: leaving the slot as it is would hold its other pages for good.
 __global__ void __launch_bounds__(256) cache_free_kernel(const ServeCache c, const int32_t *slots, int *status) {
     grid_dependency_wait();
     const int i = blockIdx.x;

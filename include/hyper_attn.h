@@ -380,7 +380,8 @@ HA_API int hyper_attn_tree(hyper_attn_t h, const ha_cache *cache, const ha_tree_
 /* The cache's steps; n entries (n = 0: nothing is done; at most 16384, append 65536), all lists in device memory. A
  * slot named twice in one call counts once (the first time) and is reported by hyper_attn_status like an entry out of
  * range.
- *   free     releases the pages of slots[i] and empties the slot.
+ *   free     releases the pages of slots[i] and empties the slot. Page numbers out of range in the slot's row are passed
+ *            over and reported; the rest of it is released all the same, so that no damage holds pages for good.
  *   fork     dst[i] (an empty slot) becomes a copy of src[i]: it shares the pages of the committed rows. Sources
  *            are read as they were before the call; a source that is also a destination is refused, and so is one
  *            with a page out of range among those.

@@ -1,5 +1,5 @@
 """The cache's steps on lists and tables that are not in order: offsets of an append that are out of range, page numbers and
-lengths that a fork must not take over."""
+lengths that a fork must not take over, and what a free does with them."""
 import pytest
 
 from approximate_long_context_b200 import binding
@@ -124,3 +124,21 @@ def test_fork_of_a_damaged_length(ha, length):
     assert ha.status() == binding.HA_ERR_INVALID_ARG and ha.status() == 0
     assert c.lens.tolist() == [length, 0, 0, 0, 0] and c.held.tolist() == [3, 0, 0, 0, 0] and c.refs.tolist() == refs
     assert c.table[1].tolist() == [-1] * 4
+
+
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 10, 2 ** 31 - 1])
+def test_free_of_a_damaged_row(ha, bad):
+    """The slot is emptied and its other pages are released, so that a damaged row does not hold pages for good."""
+    c = one_sequence()
+    ha.cache_reserve(c, ints([0, 3]), ints([40, 20]))
+    ha.cache_commit(c, ints([0, 3]), ints([40, 20]))
+    assert ha.status() == 0
+    lost = c.table[0, 1].item()
+    c.table[0, 1] = bad
+    refs = c.refs.tolist()
+    for p in c.table[0, [0, 2]].tolist():
+        refs[p] -= 1
+    ha.cache_free(c, ints([0]))
+    assert ha.status() == binding.HA_ERR_INVALID_ARG and ha.status() == 0
+    assert c.table[0].tolist() == [-1] * 4 and c.lens.tolist() == [0, 0, 0, 20, 0] and c.held.tolist() == [0, 0, 0, 2, 0]
+    assert c.refs.tolist() == refs and refs[lost] == 1
