@@ -781,12 +781,16 @@ int hyper_attn_debug_copy(hyper_attn_t h, int what, int level, void *dst, size_t
 int hyper_attn_status(hyper_attn_t h) {
     if (!h) return HA_ERR_INVALID_ARG;
     DeviceGuard g(h->device);
-    HA_CUDA(h, cudaStreamSynchronize(static_cast<cudaStream_t>(h->opt.stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(h->opt.stream);
+    HA_CUDA(h, cudaStreamSynchronize(st));
+    // The serving word is taken on the handle's stream: nothing else is waited for, and no bit that a graph sets meanwhile is lost.
     int word = 0, serve = 0;
+    int *const taken = h->serve_status + hyper_attn_s::kTakenStatus;
+    if (!ha::launch_take_status(h->serve_status, taken, st)) return fail(h, HA_ERR_CUDA, "the status word could not be read");
+    HA_CUDA(h, cudaMemcpyAsync(&serve, taken, sizeof serve, cudaMemcpyDeviceToHost, st));
+    HA_CUDA(h, cudaStreamSynchronize(st));
     if (h->ws) HA_CUDA(h, cudaMemcpy(&word, h->ws + h->lay.status, sizeof word, cudaMemcpyDeviceToHost));
-    HA_CUDA(h, cudaMemcpy(&serve, h->serve_status, sizeof serve, cudaMemcpyDeviceToHost));
     if (word) HA_CUDA(h, cudaMemset(h->ws + h->lay.status, 0, sizeof word));
-    if (serve) HA_CUDA(h, cudaMemset(h->serve_status, 0, sizeof serve));
     word |= serve;
     if (word) {
         if (word & ha::kStatusTimeout) return fail(h, HA_ERR_TIMEOUT, "a device-side wait gave up (status %d)", word);

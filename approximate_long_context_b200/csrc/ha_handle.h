@@ -59,7 +59,8 @@ struct hyper_attn_s {
     std::vector<Rec> recs;
     size_t ev_used = 0;
     // status word of the serving entry points: allocated with the handle and never moved, so that a captured
-    // graph may go on writing to it
+    // graph may go on writing to it; the word kTakenStatus behind it is what hyper_attn_status took
+    static constexpr int kTakenStatus = 32;
     int *serve_status = nullptr;
     int sms = 0;
 };

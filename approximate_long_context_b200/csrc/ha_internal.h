@@ -170,6 +170,9 @@ int launch_tree_tc(const ServeArgs &a, cudaStream_t st);
 // The second kernel of a tree call on `blocks` blocks whose segments have at most `rows` query rows.
 bool launch_tree_join(const ServeArgs &a, int blocks, int rows, cudaStream_t st);
 
+// *taken = *status, *status = 0, as one step beside kernels that set bits.
+bool launch_take_status(int *status, int *taken, cudaStream_t st);
+
 size_t cache_workspace(int64_t n, int64_t pages);
 int launch_cache_free(const ServeCache &c, const int32_t *slots, int n, int *status, cudaStream_t st);
 int launch_cache_fork(const ServeCache &c, const int32_t *src, const int32_t *dst, int n, int *status, cudaStream_t st);

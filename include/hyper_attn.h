@@ -216,7 +216,8 @@ HA_API int hyper_attn_debug_copy(hyper_attn_t h, int what, int level, void *host
  * wait gave up, or HA_ERR_CUDA if the stream holds an error or (HA_DEBUG build, libhyper_attn_debug.so) a
  * tensor-core kernel read a row index out of range from a permutation or a sample list (it then read row 0
  * instead), or HA_ERR_INVALID_ARG if a serving call met an entry out of range in device memory. Clears the
- * device status words. */
+ * device status words. Graphs with serving calls may run on other streams meanwhile: what they report is in this
+ * answer or in a later one. */
 HA_API int hyper_attn_status(hyper_attn_t h);
 
 /* Kernel classes for profiling. */

@@ -1,0 +1,72 @@
+"""What the serving calls share in a handle, under capture and beside work on other streams."""
+import pytest
+
+from approximate_long_context_b200 import binding
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def busy(stream, ms=300):
+    """Keeps a stream busy for about so long; the event behind it."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(int(ms * 1.9e6))
+        return stream.record_event()
+
+
+def rows(n=40):
+    q = torch.randn(n, 2, 64, device="cuda").to(torch.bfloat16)
+    return q, torch.empty_like(q)
+
+
+def test_status_waits_for_the_handles_stream_alone():
+    """A handle that only serves asks for its status without waiting for the default stream."""
+    side = torch.cuda.Stream()
+    ha = binding.HyperAttention(0)
+    ha.set_options(dtype="bf16", stream=side.cuda_stream)
+    q, o = rows()
+    cu, bad = ints([0, 40]), ints([0, 41])
+    torch.cuda.synchronize()
+    ha.prompt(q, q, q, o, cu)
+    assert ha.status() == 0
+    end = busy(torch.cuda.default_stream())
+    assert ha.status() == 0
+    ha.prompt(q, q, q, o, bad)
+    assert ha.status() == binding.HA_ERR_INVALID_ARG and ha.status() == 0
+    assert not end.query()
+    torch.cuda.synchronize()
+    ha.close()
+
+
+def test_reports_of_a_graph_on_another_stream():
+    """A graph that always reports runs on another stream while the status is asked for: every replay that had ended before the
+    question is in the answer."""
+    side, own = torch.cuda.Stream(), torch.cuda.Stream()
+    ha = binding.HyperAttention(0)
+    q, o = rows()
+    bad = ints([0, 41])
+    torch.cuda.synchronize()
+    ha.set_options(dtype="bf16", stream=side.cuda_stream)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        ha.prompt(q, q, q, o, bad)
+    ha.set_options(dtype="bf16", stream=own.cuda_stream)
+    assert ha.status() == 0
+    asked = 0
+    for _ in range(300):
+        with torch.cuda.stream(side):
+            g.replay()
+            done = side.record_event()
+        while not done.query():
+            asked += 1
+            ha.status()
+        with torch.cuda.stream(side):
+            g.replay()
+        side.synchronize()
+        assert ha.status() == binding.HA_ERR_INVALID_ARG
+    assert ha.status() == 0
+    ha.close()
