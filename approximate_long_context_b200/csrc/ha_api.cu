@@ -13,6 +13,19 @@ constexpr int kDiagMaxN = 16384;   // the diagnostics visit every entry of A
 
 size_t align_up(size_t x, size_t a = 256) { return (x + a - 1) / a * a; }
 
+// The serving status word, cleared on a stream of its own: on the default stream the clearing could come behind the first calls
+// on the handle, and while another stream is captured that stream may not be used.
+bool make_serve_status(hyper_attn_t h) {
+    constexpr size_t bytes = 2 * hyper_attn_s::kTakenStatus * sizeof(int);
+    cudaStream_t st = nullptr;
+    if (cudaMalloc(&h->serve_status, bytes) != cudaSuccess ||
+        cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking) != cudaSuccess)
+        return false;
+    const bool ok = cudaMemsetAsync(h->serve_status, 0, bytes, st) == cudaSuccess && cudaStreamSynchronize(st) == cudaSuccess;
+    cudaStreamDestroy(st);
+    return ok;
+}
+
 // Causal recursion depth: n <= base -> 0 levels (one exact causal problem); else n = base * 2^L.
 int causal_levels(int64_t n, int64_t base, int *L) {
     if (base <= 0 || n <= 0) return -1;
@@ -453,6 +466,7 @@ int hyper_attn_version(void) { return kVersion; }
 int hyper_attn_create(hyper_attn_t *out, int device) {
     if (!out) return HA_ERR_INVALID_ARG;
     *out = nullptr;
+    RelaxedCapture relaxed;
     int count = 0;
     if (cudaGetDeviceCount(&count) != cudaSuccess || count == 0) {
         cudaGetLastError();
@@ -472,7 +486,7 @@ int hyper_attn_create(hyper_attn_t *out, int device) {
         return HA_ERR_CUDA;
     }
     h->sms = prop.multiProcessorCount;
-    if (cudaMalloc(&h->serve_status, 256) != cudaSuccess || cudaMemset(h->serve_status, 0, 256) != cudaSuccess) {
+    if (!make_serve_status(h)) {
         cudaGetLastError();
         if (h->serve_status) cudaFree(h->serve_status);
         cudaEventDestroy(h->pin_free);
@@ -848,6 +862,7 @@ int hyper_attn_destroy(hyper_attn_t h) {
     if (!h) return HA_OK;
     {
         DeviceGuard g(h->device);
+        RelaxedCapture relaxed;
         cudaStreamSynchronize(static_cast<cudaStream_t>(h->opt.stream));
         if (h->ws) cudaFree(h->ws);
         cudaFree(h->serve_status);

@@ -96,6 +96,16 @@ struct DeviceGuard {
     }
 };
 
+// While one lives, the calls of this thread that allocate or free do not end a capture that is under way somewhere else.
+class RelaxedCapture {
+public:
+    RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+    ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+
+private:
+    cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+};
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Brackets one kernel class's enqueue: an NVTX range (a no-op unless a tracing tool is attached) and, with

@@ -70,3 +70,56 @@ def test_reports_of_a_graph_on_another_stream():
         assert ha.status() == binding.HA_ERR_INVALID_ARG
     assert ha.status() == 0
     ha.close()
+
+
+def test_report_of_a_call_right_behind_the_handles_creation():
+    """The status word is cleared before hyper_attn_create returns, also when the default stream is busy."""
+    side = torch.cuda.Stream()
+    q, o = rows()
+    bad = ints([0, 41])
+    torch.cuda.synchronize()
+    busy(torch.cuda.default_stream())
+    ha = binding.HyperAttention(0)
+    ha.set_options(dtype="bf16", stream=side.cuda_stream)
+    ha.prompt(q, q, q, o, bad)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert ha.status() == binding.HA_ERR_INVALID_ARG and ha.status() == 0
+    ha.close()
+
+
+def raw_capture(stream):
+    """A capture begun and ended without torch's knowledge."""
+    runtime = pytest.importorskip("cuda.bindings.runtime")
+
+    class Capture:
+        def __enter__(self):
+            err, = runtime.cudaStreamBeginCapture(stream.cuda_stream, runtime.cudaStreamCaptureMode.cudaStreamCaptureModeGlobal)
+            assert err == runtime.cudaError_t.cudaSuccess
+            return self
+
+        def __exit__(self, *_):
+            err, graph = runtime.cudaStreamEndCapture(stream.cuda_stream)
+            self.ok = err == runtime.cudaError_t.cudaSuccess
+            if self.ok:
+                runtime.cudaGraphDestroy(graph)
+
+    return Capture()
+
+
+def test_a_handle_made_while_a_stream_is_captured():
+    """Making or closing a handle does not end a capture that is under way."""
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with raw_capture(side) as c:
+        ha = binding.HyperAttention(0)
+    assert c.ok
+    ha.set_options(dtype="bf16", stream=side.cuda_stream)
+    q, o = rows()
+    torch.cuda.synchronize()
+    ha.prompt(q, q, q, o, ints([0, 40]))
+    assert ha.status() == 0
+    with raw_capture(side) as c:
+        binding.HyperAttention(0).close()
+    assert c.ok
+    ha.close()
