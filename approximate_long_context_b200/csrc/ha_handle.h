@@ -109,12 +109,14 @@ private:
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Brackets one kernel class's enqueue: an NVTX range (a no-op unless a tracing tool is attached) and, with
-// profiling on, two events from the handle's pool (grown on demand) on the stream.
+// profiling on, two events from the handle's pool (grown on demand) on the stream. Not under capture: events recorded
+// there have no time, and no later read could pass them.
 class ProfScope {
 public:
     ProfScope(hyper_attn_t h, int cls, const char *name, cudaStream_t st) : h_(h), cls_(cls), st_(st) {
         nvtxRangePushA(name);
-        if (!h->profiling) return;
+        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+        if (!h->profiling || cudaStreamIsCapturing(st, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) return;
         while (h->ev_pool.size() < h->ev_used + 2) {
             cudaEvent_t e;
             if (cudaEventCreate(&e) != cudaSuccess) return;

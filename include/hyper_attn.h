@@ -234,7 +234,8 @@ typedef enum {
 } ha_kernel_class;
 
 /* enable = 1: record a CUDA event pair on the handle's stream around every kernel class launch of the
- * following forward calls; 0: stop recording. Recording adds two event records per launch.
+ * following forward calls; 0: stop recording. Recording adds two event records per launch. A serving call that is captured
+ * into a graph is not recorded (its kernels run with the graph).
  * Independently of this switch, the host-side enqueue of every kernel class sits in an NVTX range named
  * "ha:hash", "ha:sort", "ha:attn", "ha:causal_base", "ha:draws", "ha:prompt", "ha:tree" or "ha:cache", which tracing tools (Nsight Systems) show
  * next to the kernels; without such a tool attached the ranges cost a few nanoseconds. */

@@ -123,3 +123,27 @@ def test_a_handle_made_while_a_stream_is_captured():
         binding.HyperAttention(0).close()
     assert c.ok
     ha.close()
+
+
+def test_profile_of_eager_and_captured_calls():
+    """A captured call has no time of its own: it is not recorded, and the calls around it are."""
+    side = torch.cuda.Stream()
+    ha = binding.HyperAttention(0)
+    ha.set_options(dtype="bf16", stream=side.cuda_stream)
+    q, o = rows()
+    cu = ints([0, 40])
+    torch.cuda.synchronize()
+    ha.profile(True)
+    ha.prompt(q, q, q, o, cu)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        ha.prompt(q, q, q, o, cu)
+    ha.prompt(q, q, q, o, cu)
+    with torch.cuda.stream(side):
+        g.replay()
+    ms, launches = ha.profile_read()["prompt"]
+    assert launches == 2 and ms > 0
+    assert ha.profile_read()["prompt"] == (0.0, 0)
+    ha.profile(False)
+    assert ha.status() == 0
+    ha.close()
