@@ -254,7 +254,7 @@ class HyperAttention:
         self.device = device
         self._device_object = None
         self._ws, self._ws_ptr, self._ws_bytes = None, 0, 0
-        self._captured = []
+        self._captured, self._pooled, self._pool_freed = [], set(), -1
         self._needs = {}
 
     def _check(self, rc: int):
@@ -350,9 +350,24 @@ class HyperAttention:
                 ws = torch.empty(nbytes, dtype=torch.uint8, device=self._torch_device())
         if not capturing:
             self._ws, self._ws_ptr, self._ws_bytes = ws, ws.data_ptr(), nbytes
-        elif not torch.cuda.is_current_stream_capturing():
+        elif not self._in_graph_pool(ws.data_ptr()):
             self._captured.append(ws)   # a capture that torch does not know of: its memory is not the graph's
         return ws.data_ptr()
+
+    def _in_graph_pool(self, ptr: int) -> bool:
+        """Whether the memory at ptr is of one of torch's private pools, which a capture by torch allocates from and which lives
+        as long as its graph. An answer holds until torch gives memory back to the device."""
+        freed = _torch.cuda.memory_stats(self.device).get("segment.all.freed")
+        if freed is None:
+            return False                # another allocator than torch's own: nothing is known
+        if freed != self._pool_freed:
+            self._pool_freed = freed
+            self._pooled.clear()
+        if ptr not in self._pooled:
+            for segment in _torch.cuda.memory_snapshot(include_traces=False):
+                if 0 <= ptr - segment["address"] < segment["total_size"] and tuple(segment["segment_pool_id"]) != (0, 0):
+                    self._pooled.add(ptr)
+        return ptr in self._pooled
 
     def _torch_device(self):
         if self._device_object is None:

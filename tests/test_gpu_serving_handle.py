@@ -147,3 +147,68 @@ def test_profile_of_eager_and_captured_calls():
     ha.profile(False)
     assert ha.status() == 0
     ha.close()
+
+
+def decoding(ha):
+    c = binding.PagedCache.empty(layers=1, pages=6, kv_heads=2, page=16, d=64, slots=1, max_pages=3)
+    ha.cache_reserve(c, ints([0]), ints([20]))
+    ha.cache_commit(c, ints([0]), ints([19]))
+    q, o = rows(1)
+    slots, at = ints([0]), ints([0, 1])
+    ha.tree(q, c, o, slots, at, max_draft=1)       # eager once: the buffers' memory is there
+    torch.cuda.synchronize()
+    return lambda: ha.tree(q, c, o, slots, at, max_draft=1)
+
+
+@pytest.mark.parametrize("current", [True, False])
+def test_workspace_of_a_capture_that_torch_does_not_know_of(current):
+    """Its buffer is kept for the graph's replays; memory that torch hands out afterwards is other memory."""
+    side = torch.cuda.Stream()
+    ha = binding.HyperAttention(0)
+    ha.set_options(dtype="bf16", stream=side.cuda_stream)
+    step = decoding(ha)
+    nbytes = binding.lib().hyper_attn_tree_workspace(ha._h, 64)
+    with torch.cuda.stream(side):
+        spare = torch.empty(nbytes, dtype=torch.uint8, device="cuda")   # what the capture finds in torch's cache
+    side.synchronize()
+    del spare
+    used = []
+    real = ha._workspace
+    ha._workspace = lambda n: used.append(real(n)) or used[-1]
+    with torch.cuda.stream(side if current else torch.cuda.default_stream()):
+        with raw_capture(side) as c:
+            step()
+            step()
+    assert c.ok and len(used) == 2
+    with torch.cuda.stream(side):
+        later = [torch.empty(nbytes, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    for x in later:
+        for p in used:
+            assert x.data_ptr() + nbytes <= p or p + nbytes <= x.data_ptr()
+    ha.close()
+
+
+def test_workspaces_of_torch_graphs_are_the_graphs():
+    """Torch's own captures have the buffers in the graph's pool: nothing is kept for them in the handle, and the calls of a
+    graph, which run one after the other, have one buffer."""
+    side = torch.cuda.Stream()
+    ha = binding.HyperAttention(0)
+    ha.set_options(dtype="bf16", stream=side.cuda_stream)
+    step = decoding(ha)
+    used = []
+    real = ha._workspace
+    ha._workspace = lambda n: used.append(real(n)) or used[-1]
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            for _ in range(3):
+                step()
+        graphs.append(g)
+    assert not ha._captured
+    assert len(set(used[:3])) == 1 and len(set(used[3:])) == 1 and used[0] != used[3]
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    assert ha.status() == 0
+    ha.close()
