@@ -354,12 +354,15 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
         }
         fence_proxy_async_smem();
     }
+    if (warp == 0 && lane == 0) {
+        prefetch_map(&maps.q);
+        prefetch_map(&maps.k);
+        prefetch_map(&maps.v);
+    }
+    if (TREE || gridDim.x < a.sms) allow_dependents();
+    grid_dependency_wait();   // what was in front on the stream, the list of prompt items among it
+    // TMEM only now: a block that held it while it waits could keep it from a block of what it waits for
     if (warp == 0) {
-        if (lane == 0) {
-            prefetch_map(&maps.q);
-            prefetch_map(&maps.k);
-            prefetch_map(&maps.v);
-        }
         tmem_alloc(sbase + C::kTmemSlot, 512);
         tmem_relinquish();
     }
@@ -367,8 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1) serve_tc_kernel(const TcArgs x, c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + C::kTmemSlot);
-    if (TREE || gridDim.x < a.sms) allow_dependents();
-    grid_dependency_wait();   // what was in front on the stream, the list of prompt items among it
 
     // a wait of a whole warp: all of its lanes go on or none
     auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, bar_wait(b, parity, abort_flag)); };

@@ -212,3 +212,65 @@ def test_workspaces_of_torch_graphs_are_the_graphs():
     torch.cuda.synchronize()
     assert ha.status() == 0
     ha.close()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("captured", [False, True])
+def test_serving_calls_between_matrix_products(d, captured):
+    """A step as a model makes it: products on the tensor cores before and behind every attention call, which start early on the
+    stream. The results are those of each call on its own."""
+    side = torch.cuda.Stream()
+    ha = binding.HyperAttention(0)
+    ha.set_options(dtype="bf16", stream=side.cuda_stream)
+    g = torch.Generator(device="cuda").manual_seed(d)
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    lens, hq, hk = [300, 41, 1, 700], 8, 2
+    at = [0, 300, 341, 342, 1042]
+    x, w, out = new(1042, 512), new(512, (hq + 2 * hk) * d) / 16, new(hq * d, 512) / 16
+    c = binding.PagedCache.empty(layers=1, pages=40, kv_heads=hk, page=64, d=d, slots=4, max_pages=20)
+    cu, slots, ones = ints(at), ints([0, 1, 2, 3]), ints([0, 1, 2, 3, 4])
+    o, o1 = torch.empty(1042, hq, d, device="cuda", dtype=torch.bfloat16), torch.empty(4, hq, d, device="cuda", dtype=torch.bfloat16)
+    last = torch.tensor(at[1:], device="cuda") - 1
+    ints_lens, ints_one = ints(lens), ints([1] * 4)
+    torch.cuda.synchronize()
+
+    def heads(y):
+        y = y.view(y.shape[0], hq + 2 * hk, d)
+        return y[:, :hq], y[:, hq:hq + hk], y[:, hq + hk:]
+
+    def step(wait):
+        q, k, v = heads(x @ w)
+        wait()
+        ha.prompt(q, k, v, o, cu, max_len=700, scale=d ** -0.5)
+        wait()
+        y = o.view(1042, hq * d) @ out
+        q1, k1, v1 = heads(y[last] @ w)
+        wait()
+        ha.cache_free(c, slots)
+        ha.cache_reserve(c, slots, ints_lens)
+        ha.cache_append(c, slots, cu, k[None], v[None])
+        ha.cache_commit(c, slots, ints_lens)
+        ha.cache_reserve(c, slots, ints_one)
+        ha.cache_append(c, slots, ones, k1[None], v1[None])
+        wait()
+        ha.tree(q1, c, o1, slots, ones, max_draft=1, scale=d ** -0.5)
+        wait()
+        return y, o1.view(4, hq * d) @ out
+
+    with torch.cuda.stream(side):
+        want = [t.clone() for t in step(torch.cuda.synchronize)]
+        torch.cuda.synchronize()
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                got = step(lambda: None)
+            for _ in range(20):
+                graph.replay()
+        else:
+            for _ in range(20):
+                got = step(lambda: None)
+        torch.cuda.synchronize()
+    assert ha.status() == 0, ha.last_error()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    ha.close()
