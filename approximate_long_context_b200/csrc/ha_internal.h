@@ -152,7 +152,6 @@ struct ServeArgs {
     int page_shift;
     // workspace: prompt: the list of work items; tree: descriptors and partial results of split segments
     void *ws;
-    size_t ws_bytes;
     int sms;
 };
 

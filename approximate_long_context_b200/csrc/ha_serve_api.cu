@@ -146,7 +146,6 @@ int hyper_attn_prompt(hyper_attn_t h, const ha_prompt_args *p) {
         a.out_dtype = out_type(h);
         a.status = h->serve_status;
         a.ws = p->workspace;
-        a.ws_bytes = p->workspace_bytes;
         a.sms = h->sms;
         cudaStream_t st = static_cast<cudaStream_t>(h->opt.stream);
         ProfScope prof(h, HA_KC_PROMPT, "ha:prompt", st);
@@ -208,7 +207,6 @@ int hyper_attn_tree(hyper_attn_t h, const ha_cache *cache, const ha_tree_args *p
         a.pages = c.pages; a.max_slots = c.slots; a.max_pages = c.max_pages;
         a.page_shift = c.page_shift;
         a.ws = p->workspace;
-        a.ws_bytes = p->workspace_bytes;
         a.sms = h->sms;
         cudaStream_t st = static_cast<cudaStream_t>(h->opt.stream);
         ProfScope prof(h, HA_KC_TREE, "ha:tree", st);
