@@ -422,7 +422,8 @@ class HyperAttention:
     def tree(self, Q, cache, O, slots, offsets, *, mask=None, max_draft=64, layer=0, scale=1.0, lse=None):
         """Exact attention of drafted tokens (or single ones) over a PagedCache: sequence i (slot slots[i]; None: slot i) has
         the rows offsets[i] .. offsets[i+1]-1 of Q and O [tokens, heads, d], whose keys and values were appended behind
-        the slot's committed rows. mask [tokens] int64: bit j of a row lets it see drafted row j (None: rows 0..i)."""
+        the slot's committed rows. mask [tokens] int64: bit j of a row lets it see drafted row j (None: rows 0..i). max_draft:
+        no sequence has more rows; the kernel is chosen by it, so a bound near the truth (1 for decoding) is the faster one."""
         c = self._cache(cache)
         q, o = self._rows(Q, "Q", self.options.dtype), self._rows(O, "O", self._out_dtype())
         tokens, heads, d = shape = Q.shape

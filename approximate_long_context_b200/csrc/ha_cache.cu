@@ -8,8 +8,8 @@
 //
 // What bounds these kernels: the row traffic (each row read once and written once, 16 bytes per thread) for large
 // calls, launch latency and the chain of dependent loads (slot -> length -> page -> row) for small ones. All five steps for
-// 64 branches of 8 prompts (drafts of up to 16, 32 layers, 8 heads, d = 128): 69 us against 51 us for the rows' bytes at the
-// memory's rate; for two branches in one layer: 16.5 us, five launches.
+// 64 branches of 8 prompts (drafts of up to 16, 32 layers, 8 heads, d = 128): 68 us against 38 to 41 us for the rows' bytes at
+// the memory's rate; for two branches in one layer: 16.6 us, five launches.
 #include "ha_common.cuh"
 #include "ha_internal.h"
 #include "ha_serve.cuh"

@@ -9,7 +9,8 @@
 // in the persistent tcgen05 kernel; 256 of up to 32 tokens, 16 heads, d = 64: 26 us against 48; but 256 of up to 128
 // tokens: 71 against 52, as mma.sync multiplies at a fraction of tcgen05's rate.
 //
-// The weights are rounded to bf16 because the tensor core multiplies bf16; the normaliser sums the unrounded values.
+// The weights are rounded to bf16 because the tensor core multiplies bf16; the normaliser sums the unrounded values, and the
+// exponentials are the hardware's (ex2.approx, a few units in the last place of fp32: far below a weight's rounding).
 // Values of keys that a row does not see may be infinities or NaN: in the 16 keys at the diagonal what is not finite is
 // taken as 0, and added to the rows that see it.
 #include <math.h>

@@ -19,7 +19,9 @@
 // Per unit (tile t, key tile): S = Q K^T (128 x 128, fp32, TMEM), P = 2^(c S - m) in bf16 over the first half of S's
 // columns, O_t += P V (TMEM). A thread of the softmax owns a query row; it keeps m and l in fp32 and rescales O only when
 // the maximum grows by more than 2^8 (P stays below 2^8; the sums are fp32, so the unscaled start costs no precision).
-// P is rounded to bf16 because the tensor core multiplies bf16; l sums the unrounded values.
+// P is rounded to bf16 because the tensor core multiplies bf16; l sums the unrounded values. The exponentials and the final
+// quotient are the hardware's ex2.approx and rcp.approx: a few units in the last place of fp32, far below a weight's rounding
+// to bf16. Calls that want fp32 weights take the SIMT family.
 //
 // Issue order: S(next unit) goes out before P V(unit) is waited for when it belongs to the other tile, so a tile's P V and
 // next S run back to back while the other tile is in its softmax. A commit after S(j + 1) covers P V(j) too (same issuing
@@ -36,10 +38,11 @@
 //
 // What bounds it. Prompts: per tile and unit (128 rows x 128 keys, d = 128) the softmax takes about 1900 cycles and P V
 // with the next S another 1600, of which 1024 are the tensor pipe's; two tiles overlap, so tensor pipe and exponentials
-// are busy 59% each, and TMEM has no room for a third tile. 32768 tokens, 8 heads on 2, d = 128: 1.76 ms (1250 TFLOP/s; 2.00
-// ms under sustained power). 16 prompts of up to 2047 tokens, 32 heads on 8: 230 us (870 TFLOP/s). Prompts of one key
-// tile (256 of up to 128 tokens, 16 heads, d = 64: 53 us, 2.5 TB/s): instruction fetch, each role's code runs once per
-// item. Decoding and small trees: reading the cache, 64 users and 2.2 GB: 330 us (6.6 TB/s).
+// are busy 59% each, and TMEM has no room for a third tile. 32768 tokens, 8 heads on 2, d = 128: 2.00 ms back to back (1100
+// TFLOP/s), 1.76 ms in a burst at full clock. 16 prompts of up to 2047 tokens, 32 heads on 8: 266 us (750 TFLOP/s), 240 in a
+// burst; their items are short, and a diagonal tile costs as much as a full one. Prompts of one key tile (256 of up to 128
+// tokens, 16 heads, d = 64: 53 us, 2.5 TB/s): instruction fetch, each role's code runs once per item. Decoding and small
+// trees: reading the cache, 64 users and 2.2 GB: 332 to 357 us by the card (6.1 to 6.5 TB/s).
 #include <cuda.h>
 #include <math.h>
 

@@ -89,7 +89,8 @@ typedef struct {
 } ha_options;
 
 /* Create a handle bound to CUDA device `device`. The handle owns a grow-only device workspace (ranks,
- * permutations, per-level partial results, the draws) and a small page-locked staging buffer.
+ * permutations, per-level partial results, the draws), a small page-locked staging buffer and the status word of
+ * the serving calls. Handles may be created and destroyed while another stream is captured.
  * Fails with HA_ERR_CUDA if the device cannot be used, HA_ERR_UNSUPPORTED if it is not sm_100. */
 HA_API int hyper_attn_create(hyper_attn_t *out, int device);
 
@@ -262,7 +263,8 @@ HA_API const char *hyper_attn_last_error(hyper_attn_t h);
  * allocates again. count = 0 clears the hook. Returns HA_ERR_INVALID_ARG for a null handle or count < 0. */
 HA_API int hyper_attn_test_fail_alloc(hyper_attn_t h, int count);
 
-/* Release the workspace and the handle. NULL is accepted. Synchronises the handle's stream first. */
+/* Release the workspace and the handle. NULL is accepted. Synchronises the handle's stream first. Graphs that hold serving
+ * calls of the handle must not run any more: they write its status word. */
 HA_API int hyper_attn_destroy(hyper_attn_t h);
 
 /*
@@ -307,7 +309,8 @@ HA_API int hyper_attn_forward_noalloc(const void *Q, const void *K, const void *
  *   - Offsets, lengths, slots, masks and page tables are device memory and are read when the kernels run. An
  *     entry out of range leaves its sequence out (nothing of it is written; a page out of range in an attention call
  *     counts as rows of zeros) and makes hyper_attn_status report HA_ERR_INVALID_ARG; nothing is read or written out
- *     of bounds.
+ *     of bounds. Where an offset falls back, so that sequences on both sides of it share rows, each row of those
+ *     sequences holds a result of one of them or what it held before the call.
  *   - A row that sees nothing gives O = 0 and a log normaliser of -inf; so does one whose scores are all -inf
  *     over finite values. Infinities and NaN in keys and values that a row does not see do not reach it.
  *   - Rows of O (and of the log normalisers) behind the last sequence are left as they are.
